@@ -348,6 +348,172 @@ logmel_status logmel_partition_utterances(const int64_t* frame_offsets, int64_t 
                                           int64_t* utt_begin);
 logmel_status logmel_partition_streams(int64_t n_streams, int n_parts, int64_t* stream_begin);
 
+/* ---- Token cache: a stream's keys and values, carried from push to push --------
+ * The rows a stream emits become tokens of a decoder or of a causal audio
+ * tower, and those attend to every token the stream had before: the streaming
+ * state one layer above the sample carry of logmel_stream.  It is a paged
+ * cache of keys and values per stream ("Audio8-ASR-Infinite": a rolling key /
+ * value cache, 750 tokens of sliding window), fed by the same ragged pushes.
+ * A cache plan holds the head layout, the rotary frequencies and the scratch;
+ * the caller owns the pages, the page table and the lengths, and describes
+ * them with a logmel_cache_view.
+ *
+ * A push of new tokens goes through four calls, each of which the caller may
+ * make or leave out:
+ *   logmel_cache_append   turns queries and keys by their positions, writes
+ *                         the keys and values into the stream's pages
+ *   logmel_cache_attend   attention of the new tokens over the cached ones
+ *   logmel_cache_weigh    adds up the attention weight each cached key got
+ *   logmel_cache_evict    keeps the newest keys and those of largest weight
+ *
+ * Conventions, beside those at the top of this file:
+ *   - offsets (host, int64, n_streams + 1 entries, CSR, non-decreasing, offsets[0]
+ *     = 0): stream s's new tokens are rows offsets[s] .. offsets[s + 1] - 1 of the
+ *     row arrays (q, k, v, out, lse).  A stream may have none.  The offsets
+ *     are read during the call (they travel in the launch parameters, so a
+ *     captured call replays with the offsets it was captured with).
+ *   - lens (device, int32) counts the new tokens too: with n new tokens, token
+ *     i (0 <= i < n) is the stream's slot p = lens[s] - n + i, and append writes
+ *     its key there.  The caller advances lens before the calls (and may do
+ *     so inside a CUDA graph: the kernels read lens and the table when they run).
+ *   - Slot j of stream s lives in page table[s * table_width + j / page_size]
+ *     at row j % page_size.  Table entries past the last live page are not read.
+ *   - Token i sees slot j when j < lens[s], and j <= p if causal, and
+ *     j > p - window if window > 0 (the newest `window` tokens, itself
+ *     included).  A token that sees nothing gets a zero output row, and
+ *     minus infinity in lse.  What unseen slots hold (stale rows, NaN,
+ *     infinities) never reaches a result; a value that is not finite reaches
+ *     exactly the rows that see it.
+ *   - Rows are 16-bit floats of the plan's type.  Row arrays may be strided
+ *     (slices of a fused projection): element (t, h, d) of a logmel_rows lies
+ *     at data + t * row_stride + h * head_stride + d.  Base addresses must be
+ *     16-byte aligned and strides non-negative multiples of 8 elements; rows
+ *     and pages that are written must not overlap one another; else
+ *     LOGMEL_ERR_INVALID_ARG.  Sums, softmax statistics and weights are fp32.
+ *   - A page id outside 0 .. n_pages - 1, a length that the table cannot hold
+ *     and a slot below zero are never followed.  The kernel stores
+ *     LOGMEL_DEVICE_BAD_CACHE in the plan's device status word; rows of that
+ *     stream then hold no meaningful values, other streams are not affected.
+ *   - The plan's scratch is shared by its calls: order calls on one plan on
+ *     the GPU (one stream, or events), replayed graphs included.  The calls
+ *     allocate nothing and never synchronise, so all of them may be captured.
+ */
+typedef struct logmel_cache_plan logmel_cache_plan;
+
+#define LOGMEL_BF16 0
+#define LOGMEL_FP16 1
+#define LOGMEL_ROTARY_PLAIN 0
+#define LOGMEL_ROTARY_LINEAR 1
+#define LOGMEL_ROTARY_RAMP 2
+#define LOGMEL_DEVICE_BAD_CACHE 4
+#define LOGMEL_DEVICE_WAIT_TIMEOUT 5
+
+typedef struct {
+  int n_q_heads;        /* query heads, a multiple of n_kv_heads, at most 64 per key head */
+  int n_kv_heads;       /* key / value heads; query head h reads key head h / (n_q_heads / n_kv_heads) */
+  int head_dim;         /* 64 or 128 */
+  int page_size;        /* tokens per page: 16, 32, 64, 128 or 256 */
+  int dtype;            /* LOGMEL_BF16 or LOGMEL_FP16 */
+  int rotary_dim;       /* leading dimensions of a head that are turned: a multiple of 16, 0 .. head_dim */
+  int interleaved;      /* 0: dimension i turns with i + rotary_dim / 2; 1: with its neighbour (2 i, 2 i + 1) */
+  int rotary_scaling;   /* LOGMEL_ROTARY_* */
+  int rotary_context;   /* RAMP: the context length the frequencies were trained with */
+  double rotary_base;   /* pair i turns by position * base^(-2 i / rotary_dim) radians */
+  double rotary_factor; /* LINEAR: angles divided by it; RAMP: pairs below one turn in rotary_context are,
+                         * pairs above 32 turns are not, those between in proportion to their index, and turned
+                         * pairs are 0.1 ln(factor) + 1 times as long */
+  double softmax_scale; /* factor on q . k; 0: 1 / sqrt(head_dim) */
+} logmel_cache_config;
+
+typedef struct {
+  void* k_pages;             /* device, 16-bit; element (page, head, slot, d) at the strides below, d contiguous */
+  void* v_pages;
+  const int32_t* table;      /* device [n_streams, table_width] */
+  int32_t* lens;             /* device [n_streams] */
+  float* mass;               /* device [n_pages, n_kv_heads, page_size] contiguous, or NULL */
+  int64_t n_pages;
+  int64_t n_streams;
+  int64_t table_width;
+  int64_t k_stride[3];       /* elements from page to page, head to head, slot to slot: positive multiples of 8 */
+  int64_t v_stride[3];
+} logmel_cache_view;
+
+typedef struct {
+  void* data;
+  int64_t row_stride;
+  int64_t head_stride;
+} logmel_rows;
+
+/* Creates a cache plan on the current CUDA device (scratch for split rows,
+ * about 40 MB, and a status word).  LOGMEL_ERR_UNSUPPORTED for a head_dim,
+ * page_size, dtype, rotary_dim or head ratio outside the lists above;
+ * LOGMEL_ERR_INVALID_ARG for other bad values (rotary_base <= 1,
+ * rotary_factor < 1, rotary_context < 1 with RAMP, a negative or not finite
+ * softmax_scale). */
+logmel_status logmel_cache_plan_create(const logmel_cache_config* config, logmel_cache_plan** out);
+
+/* Frees the plan (synchronises its device first).  NULL is a no-op. */
+void logmel_cache_plan_destroy(logmel_cache_plan* plan);
+
+/* The rotary table of a configuration, host only: inv_freq (rotary_dim / 2
+ * doubles, radians per position) and the factor on the turned pairs' length. */
+logmel_status logmel_cache_rotary(const logmel_cache_config* config, double* inv_freq, double* length);
+
+/* Rotary positions and the cache write.  For every new row t: q_out[t] = q[t]
+ * turned by its position, the turned k[t] and v[t] as it is go to the row's
+ * slot.  Angles are reduced to a fraction of a turn in 64-bit fixed
+ * point, so they are exact to fp32 at any int32 position.
+ *   q, q_out    [rows, n_q_heads, head_dim]; q_out may equal q (in place) but
+ *               must not overlap it otherwise
+ *   k, v        [rows, n_kv_heads, head_dim]
+ *   positions   device int32 [rows], >= 0, or NULL: a row's position is its slot */
+logmel_status logmel_cache_append(logmel_cache_plan* plan, const logmel_cache_view* cache, const int64_t* offsets,
+                                  const logmel_rows* q, const logmel_rows* k, const logmel_rows* v,
+                                  const int32_t* positions, const logmel_rows* q_out, void* stream);
+
+/* Attention of the new rows over the cached slots: out[t, h] = sum_j w_j v_j,
+ * w = softmax over the seen slots j of softmax_scale * q[t, h] . k_j.
+ *   q, out      [rows, n_q_heads, head_dim]; must not overlap
+ *   lse         device fp32 [rows, n_q_heads] (contiguous) or NULL: ln of the
+ *               sum of exp(softmax_scale * q . k_j)
+ * Weights are rounded to the rows' type before the product with v (as the
+ * tensor cores take them); their sum is taken in fp32 before that. */
+logmel_status logmel_cache_attend(logmel_cache_plan* plan, const logmel_cache_view* cache, const int64_t* offsets,
+                                  const logmel_rows* q, const logmel_rows* out, float* lse, int causal,
+                                  int64_t window, void* stream);
+
+/* Accumulated attention weight: for every stream with new rows and every
+ * slot j < lens[s], mass_out = decay * mass + sum over the stream's new rows t
+ * that see j, and the query heads h of the key head, of
+ * exp(softmax_scale * q[t, h] . k_j - lse[t, h]).  Streams without new rows are
+ * left as they are.  The sums are taken in a fixed order: the same
+ * call gives the same bits.
+ *   q, lse      as logmel_cache_attend took and gave them
+ *   mass_out    device, laid out as cache->mass (which must not be NULL); may
+ *               be cache->mass itself, must not overlap it otherwise */
+logmel_status logmel_cache_weigh(logmel_cache_plan* plan, const logmel_cache_view* cache, const int64_t* offsets,
+                                 const logmel_rows* q, const float* lse, int causal, int64_t window, float decay,
+                                 float* mass_out, void* stream);
+
+/* Eviction by accumulated weight: of stream s's L = lens[s] slots, min(L,
+ * budget) are kept per key head: the newest min(L, recent), and of the others
+ * those of largest mass (ties: the lowest slot; NaN counts as largest).
+ * Their keys, values and masses are written in slot order to slots 0, 1, ...
+ * of `to`, to->lens[s] = min(L, budget) is set, and kept (device int32
+ * [n_streams, n_kv_heads, budget]) receives their old slots, ascending, then -1.
+ * `to` has the same n_streams, its own table, and lens other than cache->lens;
+ * it may use pages of the same pool that no stream of `cache` has in use (a
+ * page both read and written is a race).  Both views need mass.
+ * LOGMEL_ERR_INVALID_ARG unless 1 <= budget <= to's table_width * page_size and
+ * 0 <= recent <= budget. */
+logmel_status logmel_cache_evict(logmel_cache_plan* plan, const logmel_cache_view* cache,
+                                 const logmel_cache_view* to, int64_t budget, int64_t recent, int32_t* kept,
+                                 void* stream);
+
+/* Reads and clears the plan's device status word (synchronises `stream`):
+ * 0, LOGMEL_DEVICE_BAD_CACHE or LOGMEL_DEVICE_WAIT_TIMEOUT. */
+logmel_status logmel_cache_device_status(logmel_cache_plan* plan, int* code, void* stream);
+
 /* Test hook for the bounded wait on a tile's span copies (not for normal
  * use; no page defines it).  Offline tiles staged by bulk copies wait on a
  * shared-memory barrier, polling at most poll_limit times (0: the default

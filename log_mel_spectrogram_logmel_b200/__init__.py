@@ -17,6 +17,14 @@ library has not been built (``python log_mel_spectrogram_logmel_b200/build.py``)
     windows = lm.stream_windows(frames_so_far, finished=False)      # 500-frame chunks, +-50 context
 
     lm.compute_noalloc(pcm_cuda_f32, offsets_int64, out)  # no device allocation (fixed scratch)
+
+    cp = lm.CachePlan(16, 8, 128, page_size=64, rotary_dim=128)     # 16 query heads over 8 key heads of 128
+    cache = lm.TokenCache.empty(cp, n_streams=64, max_tokens=4096)  # paged keys and values of 64 streams
+    cache.lens.add_(1)                                # one new token per stream (q, k, v: [64, heads, 128] bf16)
+    q = cache.append(q, k, v)                         # rotary positions, keys and values into the pages
+    out, lse = cache.attend(q, return_lse=True)       # attention over everything cached
+    cache.weigh(q, lse)                               # accumulated weight of every cached key
+    cache.evict(smaller, budget=750, recent=250)      # the newest and the heaviest keys, into another TokenCache
 """
 from __future__ import annotations
 
@@ -25,7 +33,7 @@ import os
 
 import numpy as np
 
-__all__ = ["Plan", "Stream", "LogMelError", "compute_noalloc", "encoder_chunks", "stream_windows", "chunk_views",
+__all__ = ["Plan", "Stream", "CachePlan", "TokenCache", "LogMelError", "compute_noalloc", "encoder_chunks", "stream_windows", "chunk_views",
            "partition_utterances", "partition_streams", "lib_path", "exported_symbols", "STATUS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -57,6 +65,24 @@ _lib = ctypes.CDLL(_LIB_PATH)
 
 _p, _i, _i64, _f, _vp = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 _i64p = ctypes.POINTER(ctypes.c_int64)
+
+
+class _CacheConfig(ctypes.Structure):
+    _fields_ = [("n_q_heads", _i), ("n_kv_heads", _i), ("head_dim", _i), ("page_size", _i), ("dtype", _i),
+                ("rotary_dim", _i), ("interleaved", _i), ("rotary_scaling", _i), ("rotary_context", _i),
+                ("rotary_base", ctypes.c_double), ("rotary_factor", ctypes.c_double),
+                ("softmax_scale", ctypes.c_double)]
+
+
+class _CacheView(ctypes.Structure):
+    _fields_ = [("k_pages", _vp), ("v_pages", _vp), ("table", _vp), ("lens", _vp), ("mass", _vp), ("n_pages", _i64),
+                ("n_streams", _i64), ("table_width", _i64), ("k_stride", _i64 * 3), ("v_stride", _i64 * 3)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", _vp), ("row_stride", _i64), ("head_stride", _i64)]
+
+
 _SIGS = {
     "logmel_status_string": (ctypes.c_char_p, [_i]),
     "logmel_last_error": (ctypes.c_char_p, []),
@@ -87,6 +113,14 @@ _SIGS = {
     "logmel_stream_windows": (_i, [_i64, _i, _i64, _i64, _vp, _i64, _i64p]),
     "logmel_partition_utterances": (_i, [_i64p, _i64, _i, _i64p]),
     "logmel_partition_streams": (_i, [_i64, _i, _i64p]),
+    "logmel_cache_plan_create": (_i, [_vp, ctypes.POINTER(_p)]),
+    "logmel_cache_plan_destroy": (None, [_p]),
+    "logmel_cache_rotary": (_i, [_vp, _vp, _vp]),
+    "logmel_cache_append": (_i, [_p, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "logmel_cache_attend": (_i, [_p, _vp, _vp, _vp, _vp, _vp, _i, _i64, _vp]),
+    "logmel_cache_weigh": (_i, [_p, _vp, _vp, _vp, _vp, _i, _i64, _f, _vp, _vp]),
+    "logmel_cache_evict": (_i, [_p, _vp, _vp, _i64, _i64, _vp, _vp]),
+    "logmel_cache_device_status": (_i, [_p, ctypes.POINTER(_i), _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -424,3 +458,260 @@ class Stream:
     def reset(self, stream_id: int = -1, stream=None) -> None:
         _check(_lib.logmel_stream_reset(self._h, stream_id, _stream_handle(stream, self.plan.device)),
                "logmel_stream_reset")
+
+
+class CachePlan:
+    """Head layout, rotary frequencies and scratch of token caches on one CUDA
+    device (logmel_cache_plan_create).  Query head h reads key head
+    h // (n_q_heads // n_kv_heads).  The leading rotary_dim dimensions of a head are
+    turned by position (default: none), dimension i with i + rotary_dim / 2
+    or, if interleaved, with its neighbour; rotary_scaling is None, "linear"
+    (angles divided by rotary_factor) or "ramp" (by wavelength, for a model
+    trained on rotary_context positions).  softmax_scale defaults to head_dim ** -0.5.
+
+    Calls on one plan share its scratch: order them on the GPU."""
+
+    _SCALINGS = {None: 0, "linear": 1, "ramp": 2}
+
+    def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int = 64, dtype=None,
+                 rotary_dim: int = 0, rotary_base: float = 10000.0, interleaved: bool = False, rotary_scaling=None,
+                 rotary_factor: float = 1.0, rotary_context: int = 0, softmax_scale=None, device=None):
+        torch = _torch()
+        self.dtype = torch.bfloat16 if dtype is None else dtype
+        if self.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("dtype must be torch.bfloat16 or torch.float16")
+        if rotary_scaling not in self._SCALINGS:
+            raise ValueError('rotary_scaling must be None, "linear" or "ramp"')
+        if softmax_scale is not None and not softmax_scale > 0:
+            raise ValueError("softmax_scale must be positive")
+        self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size = n_q_heads, n_kv_heads, head_dim, page_size
+        self._config = _CacheConfig(n_q_heads, n_kv_heads, head_dim, page_size,
+                                    0 if self.dtype == torch.bfloat16 else 1, rotary_dim, int(bool(interleaved)),
+                                    self._SCALINGS[rotary_scaling], rotary_context, rotary_base, rotary_factor,
+                                    softmax_scale or 0.0)
+        self.rotary_dim = rotary_dim
+        self.inv_freq, self.rotary_length = self._rotary()   # checks the configuration before any CUDA call
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        h = _p()
+        with torch.cuda.device(self.device):
+            _check(_lib.logmel_cache_plan_create(ctypes.addressof(self._config), ctypes.byref(h)),
+                   "logmel_cache_plan_create")
+        self._h = h
+        self._destroy = _lib.logmel_cache_plan_destroy   # kept: module globals may be gone at exit
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value:
+            self._destroy(h)
+            self._h = None
+
+    def _rotary(self):
+        inv = np.zeros(max(self.rotary_dim // 2, 1), np.float64)
+        length = ctypes.c_double(1.0)
+        if self.rotary_dim > 2 * 64:
+            _check(2, "logmel_cache_rotary")
+        _check(_lib.logmel_cache_rotary(ctypes.addressof(self._config), inv.ctypes.data, ctypes.addressof(length)),
+               "logmel_cache_rotary")
+        return inv[:self.rotary_dim // 2], length.value
+
+    def device_status(self, stream=None) -> int:
+        """Reads and clears the status word (logmel_cache_device_status): 4 when a
+        call met a page id or a length it could not follow, 5 when a wait ran out."""
+        code = ctypes.c_int(0)
+        _check(_lib.logmel_cache_device_status(self._h, ctypes.byref(code), _stream_handle(stream, self.device)),
+               "logmel_cache_device_status")
+        return code.value
+
+
+class TokenCache:
+    """Paged keys and values of n_streams streams (logmel_cache_view): the
+    streaming state of an attention layer.  The tensors are the caller's:
+
+      k_pages, v_pages  [n_pages, n_kv_heads, page_size, head_dim] of the plan's dtype, any strides that are multiples
+                        of 8 elements with contiguous head_dim (views of other orders are fine)
+      table             int32 [n_streams, width]: slot j is row j % page_size of page table[s, j // page_size]
+      lens              int32 [n_streams]: tokens of each stream, those of the push under way included
+      mass              float32 [n_pages, n_kv_heads, page_size]: accumulated weights (weigh, evict)
+
+    lens, table and mass may be changed in place between calls (also inside a CUDA graph)."""
+
+    def __init__(self, plan: CachePlan, k_pages, v_pages, table, lens, mass=None):
+        torch = _torch()
+        self.plan = plan
+        for name, t, dtype, dim in (("k_pages", k_pages, plan.dtype, 4), ("v_pages", v_pages, plan.dtype, 4),
+                                    ("table", table, torch.int32, 2), ("lens", lens, torch.int32, 1),
+                                    ("mass", mass, torch.float32, 3)):
+            if t is None and name == "mass":
+                continue
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+                raise TypeError(f"{name} must be a CUDA {dtype} tensor")
+            if t.device != plan.device:
+                raise ValueError(f"{name} is on {t.device}, the plan on {plan.device}")
+            if t.dim() != dim:
+                raise ValueError(f"{name} must have {dim} dimensions")
+            if dim < 4 and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        shape = (k_pages.shape[0], plan.n_kv_heads, plan.page_size, plan.head_dim)
+        if tuple(k_pages.shape) != shape or tuple(v_pages.shape) != shape:
+            raise ValueError(f"k_pages and v_pages must be [n_pages, {shape[1]}, {shape[2]}, {shape[3]}]")
+        if k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+            raise ValueError("the head dimension of k_pages and v_pages must be contiguous")
+        if mass is not None and tuple(mass.shape) != shape[:3]:
+            raise ValueError("mass must be [n_pages, n_kv_heads, page_size]")
+        if table.shape[0] != lens.shape[0]:
+            raise ValueError("table and lens must have one row per stream")
+        self.k_pages, self.v_pages, self.table, self.lens, self.mass = k_pages, v_pages, table, lens, mass
+        self.n_streams = lens.shape[0]
+        # sizes of one have no stride of their own: one that overlaps nothing stands in
+        def strides(t):
+            whole = [plan.n_kv_heads * plan.page_size * plan.head_dim, plan.page_size * plan.head_dim, plan.head_dim]
+            return (_i64 * 3)(*(st if n > 1 else w for st, n, w in zip(t.stride()[:3], t.shape, whole)))
+        self._view = _CacheView(k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                                mass.data_ptr() if mass is not None else None, shape[0], self.n_streams,
+                                table.shape[1], strides(k_pages), strides(v_pages))
+        self._view_ptr = ctypes.addressof(self._view)
+
+    @classmethod
+    def empty(cls, plan: CachePlan, n_streams: int, max_tokens: int) -> "TokenCache":
+        """A cache with pages of its own for max_tokens tokens of every stream, all streams empty."""
+        torch = _torch()
+        width = max(1, -(-max_tokens // plan.page_size))
+        pages = max(1, n_streams * width)
+        shape = (pages, plan.n_kv_heads, plan.page_size, plan.head_dim)
+        k = torch.empty(shape, dtype=plan.dtype, device=plan.device)
+        table = torch.arange(n_streams * width, dtype=torch.int32, device=plan.device).view(n_streams, width)
+        return cls(plan, k, torch.empty_like(k), table,
+                   torch.zeros(n_streams, dtype=torch.int32, device=plan.device),
+                   torch.zeros(shape[:3], dtype=torch.float32, device=plan.device))
+
+    def _offsets(self, offsets, rows):
+        if offsets is None:
+            if rows % max(self.n_streams, 1):
+                raise ValueError(f"{rows} rows are not the same number for each of {self.n_streams} streams")
+            n = rows // max(self.n_streams, 1)
+            return np.arange(self.n_streams + 1, dtype=np.int64) * n
+        off = _offsets(offsets)
+        if off.shape[0] != self.n_streams + 1:
+            raise ValueError("offsets must hold n_streams + 1 entries")
+        if off[0] != 0 or off[-1] != rows:
+            raise ValueError(f"offsets must run from 0 to the {rows} rows given")
+        return off
+
+    def _rows(self, t, heads, name, rows=None):
+        plan = self.plan
+        if not isinstance(t, _torch().Tensor) or not t.is_cuda or t.dtype != plan.dtype:
+            raise TypeError(f"{name} must be a CUDA {plan.dtype} tensor")
+        if t.device != plan.device:
+            raise ValueError(f"{name} is on {t.device}, the plan on {plan.device}")
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != plan.head_dim or rows not in (None, shape[0]):
+            raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {heads}, {plan.head_dim}]")
+        st = t.stride()
+        if st[2] != 1:
+            raise ValueError(f"the head dimension of {name} must be contiguous")
+        # strides of dimensions of size one are never used
+        return _Rows(t.data_ptr(), st[0] if shape[0] > 1 else heads * plan.head_dim, st[1] if heads > 1 else plan.head_dim)
+
+    def _new(self, like, heads, stream):
+        torch = _torch()
+        out = torch.empty((like.shape[0], heads, self.plan.head_dim), dtype=self.plan.dtype, device=self.plan.device)
+        if stream is not None:
+            out.record_stream(stream)
+        return out
+
+    def append(self, q, k, v, offsets=None, positions=None, q_out=None, stream=None):
+        """Turns the new rows' queries and keys by their positions, and writes
+        keys and values to the streams' newest slots (logmel_cache_append).  q is
+        [rows, n_q_heads, head_dim], k and v [rows, n_kv_heads, head_dim] (slices of a
+        fused projection are fine); offsets (host, [n_streams + 1]) cut the
+        rows into streams, default the same number each; positions (CUDA
+        int32 [rows]) default to the rows' slots.  Returns the turned queries
+        (q_out, which may be q)."""
+        torch, plan = _torch(), self.plan
+        rq = self._rows(q, plan.n_q_heads, "q")
+        rows = q.shape[0]
+        rk, rv = self._rows(k, plan.n_kv_heads, "k", rows), self._rows(v, plan.n_kv_heads, "v", rows)
+        off = self._offsets(offsets, rows)
+        pos = None
+        if positions is not None:
+            if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or positions.device != plan.device:
+                raise TypeError("positions must be an int32 tensor on the plan's device")
+            if positions.shape != (rows,) or not positions.is_contiguous():
+                raise ValueError("positions must hold one contiguous entry per row")
+            pos = positions.data_ptr()
+        if q_out is None:
+            q_out = self._new(q, plan.n_q_heads, stream)
+        ro = self._rows(q_out, plan.n_q_heads, "q_out", rows)
+        _check(_lib.logmel_cache_append(plan._h, self._view_ptr, off.ctypes.data, ctypes.addressof(rq),
+                                        ctypes.addressof(rk), ctypes.addressof(rv), pos, ctypes.addressof(ro),
+                                        _stream_handle(stream, plan.device)), "logmel_cache_append")
+        return q_out
+
+    def attend(self, q, offsets=None, causal: bool = True, window: int = 0, out=None, return_lse: bool = False,
+               stream=None):
+        """Attention of the new rows over the cached slots (logmel_cache_attend):
+        [rows, n_q_heads, head_dim], and with return_lse also the logarithm of each
+        row's sum, float32 [rows, n_q_heads].  window > 0 limits every row to
+        the newest `window` slots up to its own."""
+        torch, plan = _torch(), self.plan
+        rq = self._rows(q, plan.n_q_heads, "q")
+        rows = q.shape[0]
+        off = self._offsets(offsets, rows)
+        if out is None:
+            out = self._new(q, plan.n_q_heads, stream)
+        ro = self._rows(out, plan.n_q_heads, "out", rows)
+        lse = None
+        if return_lse:
+            lse = torch.empty((rows, plan.n_q_heads), dtype=torch.float32, device=plan.device)
+            if stream is not None:
+                lse.record_stream(stream)
+        _check(_lib.logmel_cache_attend(plan._h, self._view_ptr, off.ctypes.data, ctypes.addressof(rq),
+                                        ctypes.addressof(ro), lse.data_ptr() if return_lse else None,
+                                        int(bool(causal)), int(window), _stream_handle(stream, plan.device)),
+               "logmel_cache_attend")
+        return (out, lse) if return_lse else out
+
+    def weigh(self, q, lse, offsets=None, causal: bool = True, window: int = 0, decay: float = 1.0, out=None,
+              stream=None):
+        """Adds the attention weight that the cached keys received from the
+        new rows (logmel_cache_weigh): out = decay * mass + the weights, for every live
+        slot of the streams with new rows.  out defaults to mass itself."""
+        torch, plan = _torch(), self.plan
+        if self.mass is None:
+            raise ValueError("the cache has no mass tensor")
+        rq = self._rows(q, plan.n_q_heads, "q")
+        rows = q.shape[0]
+        off = self._offsets(offsets, rows)
+        _check_cuda_f32(lse, "lse", plan.device)
+        if lse.shape != (rows, plan.n_q_heads):
+            raise ValueError(f"lse must be [{rows}, {plan.n_q_heads}]")
+        if out is None:
+            out = self.mass
+        else:
+            _check_cuda_f32(out, "out", plan.device)
+            if out.shape != self.mass.shape:
+                raise ValueError("out must have the shape of mass")
+        _check(_lib.logmel_cache_weigh(plan._h, self._view_ptr, off.ctypes.data, ctypes.addressof(rq), lse.data_ptr(),
+                                       int(bool(causal)), int(window), float(decay), out.data_ptr(),
+                                       _stream_handle(stream, plan.device)), "logmel_cache_weigh")
+        return out
+
+    def evict(self, to: "TokenCache", budget: int, recent: int = 0, stream=None):
+        """Keeps at most budget slots of every stream and key head, the newest
+        `recent` and of the others the heaviest, and writes them in order
+        into `to` (logmel_cache_evict), whose lens and mass are set too.  Returns their
+        old slots, int32 [n_streams, n_kv_heads, budget], padded with -1."""
+        torch, plan = _torch(), self.plan
+        if not isinstance(to, TokenCache):
+            raise TypeError("to must be a TokenCache")
+        a, b = plan, to.plan
+        if (b.device, b.dtype, b.n_kv_heads, b.head_dim, b.page_size) != (a.device, a.dtype, a.n_kv_heads, a.head_dim, a.page_size):
+            raise ValueError("to must have the layout of this cache")
+        kept = torch.empty((self.n_streams, plan.n_kv_heads, max(int(budget), 0)), dtype=torch.int32, device=plan.device)
+        if stream is not None:
+            kept.record_stream(stream)
+        _check(_lib.logmel_cache_evict(plan._h, self._view_ptr, to._view_ptr, int(budget), int(recent),
+                                       kept.data_ptr(), _stream_handle(stream, plan.device)), "logmel_cache_evict")
+        return kept

@@ -15,15 +15,17 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "liblogmel_b200.so")
 SOURCES = [os.path.join(PKG, "csrc", "logmel.cu"), os.path.join(PKG, "csrc", "chunk_map.cpp"),
-           os.path.join(PKG, "csrc", "partition.cpp")]
-DEPS = SOURCES + [os.path.join(PKG, "csrc", "logmel_kernel.cuh"), os.path.join(PKG, "csrc", "mel_layout_default.h"),
-                  os.path.join(ROOT, "include", "logmel.h")]
+           os.path.join(PKG, "csrc", "partition.cpp"), os.path.join(PKG, "csrc", "cache.cu")]
+DEPS = SOURCES + [os.path.join(PKG, "csrc", name) for name in (
+    "logmel_kernel.cuh", "mel_layout_default.h", "internal.h", "cache_common.cuh", "cache_rows.cuh", "cache_attend.cuh",
+    "cache_weigh.cuh")] + [os.path.join(ROOT, "include", "logmel.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared",
     "-Xptxas", "-v",
+    "--threads", "0",
 ]
 
 

@@ -1,0 +1,461 @@
+// C ABI of the token cache (declared in include/logmel.h): argument checks,
+// the rotary table, launch shapes.  Device side: cache_rows.cuh (append,
+// evict), cache_attend.cuh, cache_weigh.cuh.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <limits>
+#include <new>
+
+#include "cache_attend.cuh"
+#include "cache_common.cuh"
+#include "cache_rows.cuh"
+#include "cache_weigh.cuh"
+#include "internal.h"
+#include "logmel.h"
+
+using namespace logmel;
+using namespace logmel::cache;
+
+struct logmel_cache_plan {
+  logmel_cache_config cfg{};
+  int device = 0, sms = 0, page_shift = 0, group = 1;
+  float scale = 0.f;
+  RotaryArgs rotary{};
+  int* d_status = nullptr;
+};
+
+namespace {
+
+#define CK(call)                                                                                \
+  do {                                                                                          \
+    cudaError_t e_ = (call);                                                                    \
+    if (e_ != cudaSuccess) return record_cuda_error(e_, #call, "cache.cu", __LINE__);           \
+  } while (0)
+
+// Makes the plan's device current for the call's launches and puts the
+// caller's back.
+class DeviceScope {
+ public:
+  explicit DeviceScope(int device) {
+    if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
+    if (prev_ != device) err_ = cudaSetDevice(device);
+    else prev_ = -1;
+  }
+  ~DeviceScope() {
+    if (prev_ >= 0) cudaSetDevice(prev_);
+  }
+  cudaError_t error() const { return err_; }
+
+ private:
+  int prev_ = -1;
+  cudaError_t err_ = cudaSuccess;
+};
+
+logmel_status check_config(const logmel_cache_config& c) {
+  if (c.n_q_heads < 1 || c.n_kv_heads < 1) return LOGMEL_ERR_INVALID_ARG;
+  if (c.n_q_heads % c.n_kv_heads || c.n_q_heads / c.n_kv_heads > 64) return LOGMEL_ERR_UNSUPPORTED;
+  if (c.n_q_heads > 4096) return LOGMEL_ERR_UNSUPPORTED;
+  if (c.head_dim != 64 && c.head_dim != 128) return LOGMEL_ERR_UNSUPPORTED;
+  if (c.page_size < 16 || c.page_size > 256 || (c.page_size & (c.page_size - 1))) return LOGMEL_ERR_UNSUPPORTED;
+  if (c.dtype != LOGMEL_BF16 && c.dtype != LOGMEL_FP16) return LOGMEL_ERR_UNSUPPORTED;
+  if (c.rotary_dim < 0 || c.rotary_dim > c.head_dim || c.rotary_dim % 16) return LOGMEL_ERR_UNSUPPORTED;
+  if (c.rotary_scaling < LOGMEL_ROTARY_PLAIN || c.rotary_scaling > LOGMEL_ROTARY_RAMP) return LOGMEL_ERR_UNSUPPORTED;
+  if (!(c.rotary_base > 1.0) || !std::isfinite(c.rotary_base)) return LOGMEL_ERR_INVALID_ARG;
+  if (c.rotary_scaling != LOGMEL_ROTARY_PLAIN && (!(c.rotary_factor >= 1.0) || !std::isfinite(c.rotary_factor)))
+    return LOGMEL_ERR_INVALID_ARG;
+  if (c.rotary_scaling == LOGMEL_ROTARY_RAMP && c.rotary_context < 1) return LOGMEL_ERR_INVALID_ARG;
+  if (!(c.softmax_scale >= 0.0) || !std::isfinite(c.softmax_scale)) return LOGMEL_ERR_INVALID_ARG;
+  return LOGMEL_OK;
+}
+
+// Radians per position of every pair.  RAMP (interpolation by wavelength, "YaRN: Efficient Context
+// Window Extension of Large Language Models", section 3.2): with r(i) = rotary_context f_i / 2 pi the turns of pair i in the
+// trained context, pairs with r >= 32 keep their frequency, pairs with r <= 1 are slowed by the factor; the
+// bounds are taken as (rounded outwards) indices, and the mix is linear in the index between them.
+void rotary_table(const logmel_cache_config& c, double* inv, double* length) {
+  const int pairs = c.rotary_dim / 2;
+  *length = 1.0;
+  for (int i = 0; i < pairs; ++i) inv[i] = std::pow(c.rotary_base, -2.0 * i / c.rotary_dim);
+  if (c.rotary_scaling == LOGMEL_ROTARY_LINEAR) {
+    for (int i = 0; i < pairs; ++i) inv[i] /= c.rotary_factor;
+  } else if (c.rotary_scaling == LOGMEL_ROTARY_RAMP) {
+    auto index_of = [&](double turns) {
+      return c.rotary_dim * std::log(c.rotary_context / (turns * 2.0 * M_PI)) / (2.0 * std::log(c.rotary_base));
+    };
+    const double low = std::max(std::floor(index_of(32.0)), 0.0);
+    const double high = std::min(std::ceil(index_of(1.0)), c.rotary_dim - 1.0);
+    for (int i = 0; i < pairs; ++i) {
+      const double slow = std::min(std::max((i - low) / std::max(high - low, 0.001), 0.0), 1.0);
+      inv[i] = inv[i] * (1.0 - slow) + inv[i] / c.rotary_factor * slow;
+    }
+    *length = 0.1 * std::log(c.rotary_factor) + 1.0;
+  }
+}
+
+bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uint64_t)nb && y < x + (uint64_t)na;
+}
+
+// Whether the elements of an array with contiguous last dimension `d` and these dimensions (sizes, strides) are all distinct.
+bool distinct(int64_t d, int dims, const int64_t* size, const int64_t* stride) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + dims, [&](int a, int b) { return stride[a] < stride[b]; });
+  int64_t extent = d;
+  for (int i = 0; i < dims; ++i) {
+    const int x = order[i];
+    if (size[x] <= 1) continue;
+    if (stride[x] < extent) return false;
+    extent += (size[x] - 1) * stride[x];
+  }
+  return true;
+}
+
+logmel_status check_rows(const logmel_cache_plan* p, const logmel_rows* r, int64_t rows, int heads, bool output) {
+  if (!r) return LOGMEL_ERR_INVALID_ARG;
+  if (r->row_stride < 0 || r->head_stride < 0 || r->row_stride % 8 || r->head_stride % 8) return LOGMEL_ERR_INVALID_ARG;
+  if (rows == 0) return LOGMEL_OK;
+  if (!r->data || misaligned(r->data, 16)) return LOGMEL_ERR_INVALID_ARG;
+  // products of sizes and strides stay far inside 64 bits
+  const int64_t limit = int64_t(1) << 38;
+  if (r->row_stride > limit / std::max<int64_t>(rows, 1) || r->head_stride > limit / heads) return LOGMEL_ERR_INPUT_TOO_LONG;
+  const int64_t size[2] = {rows, heads}, stride[2] = {r->row_stride, r->head_stride};
+  return output && !distinct(p->cfg.head_dim, 2, size, stride) ? LOGMEL_ERR_INVALID_ARG : LOGMEL_OK;
+}
+
+logmel_status check_view(const logmel_cache_plan* p, const logmel_cache_view* v) {
+  if (!p || !v) return LOGMEL_ERR_INVALID_ARG;
+  if (v->n_streams < 0 || v->table_width < 1 || v->n_pages < 1) return LOGMEL_ERR_INVALID_ARG;
+  if (v->n_streams > INT32_MAX / 2 || v->n_pages > INT32_MAX / 2 || v->table_width > INT32_MAX / 2)
+    return LOGMEL_ERR_INPUT_TOO_LONG;
+  if (!v->k_pages || !v->v_pages || misaligned(v->k_pages, 16) || misaligned(v->v_pages, 16))
+    return LOGMEL_ERR_INVALID_ARG;
+  if (v->n_streams > 0 && (!v->table || !v->lens)) return LOGMEL_ERR_INVALID_ARG;
+  if (misaligned(v->table, 4) || misaligned(v->lens, 4) || misaligned(v->mass, 16)) return LOGMEL_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (v->k_stride[i] < 8 || v->k_stride[i] % 8 || v->v_stride[i] < 8 || v->v_stride[i] % 8)
+      return LOGMEL_ERR_INVALID_ARG;
+    const int64_t limit = (int64_t(1) << 38) / (i == 0 ? v->n_pages : 4096);
+    if (v->k_stride[i] > limit || v->v_stride[i] > limit) return LOGMEL_ERR_INPUT_TOO_LONG;
+  }
+  const int64_t size[3] = {v->n_pages, p->cfg.n_kv_heads, p->cfg.page_size};
+  if (!distinct(p->cfg.head_dim, 3, size, v->k_stride) || !distinct(p->cfg.head_dim, 3, size, v->v_stride))
+    return LOGMEL_ERR_INVALID_ARG;
+  return LOGMEL_OK;
+}
+
+logmel_status check_offsets(const int64_t* off, int64_t streams, int64_t* rows) {
+  if (!off || off[0] != 0) return LOGMEL_ERR_INVALID_ARG;
+  for (int64_t s = 0; s < streams; ++s)
+    if (off[s + 1] < off[s]) return LOGMEL_ERR_INVALID_ARG;
+  *rows = off[streams];
+  return *rows > INT32_MAX / 256 ? LOGMEL_ERR_INPUT_TOO_LONG : LOGMEL_OK;
+}
+
+CacheView device_view(const logmel_cache_plan* p, const logmel_cache_view& v) {
+  CacheView c{};
+  c.k = (char*)v.k_pages;
+  c.v = (char*)v.v_pages;
+  c.table = v.table;
+  c.lens = v.lens;
+  c.mass = v.mass;
+  c.k_page = v.k_stride[0];
+  c.k_head = v.k_stride[1];
+  c.k_slot = v.k_stride[2];
+  c.v_page = v.v_stride[0];
+  c.v_head = v.v_stride[1];
+  c.v_slot = v.v_stride[2];
+  c.n_pages = (int)v.n_pages;
+  c.width = (int)v.table_width;
+  c.capacity = (int)std::min<int64_t>(v.table_width << p->page_shift, (INT32_MAX >> 1) & ~255);
+  c.page_shift = p->page_shift;
+  c.status = p->d_status;
+  return c;
+}
+
+Rows device_rows(const logmel_rows& r, int64_t first) {
+  return Rows{(char*)r.data + 2 * first * r.row_stride, r.row_stride, r.head_stride};
+}
+
+// Cuts a call into launches: runs of streams whose offsets fit a Batch.
+struct Launches {
+  const int64_t* off;
+  int64_t streams, at = 0;
+
+  bool next(Batch* b, int64_t* first_stream, int64_t* first_row) {
+    while (at < streams) {
+      const int64_t s0 = at, n0 = off[s0 + 1] - off[s0];
+      int64_t e = s0;
+      while (e < streams && e - s0 < MAX_UNIFORM && off[e + 1] - off[e] == n0) ++e;
+      const bool uniform = n0 > 0 && (e == streams || e - s0 > MAX_RAGGED);
+      if (!uniform) e = std::min<int64_t>(streams, s0 + MAX_RAGGED);
+      at = e;
+      if (off[e] == off[s0]) continue;   // nothing new in these streams
+      b->streams = (int)(e - s0);
+      b->rows = (int)(off[e] - off[s0]);
+      b->uniform = uniform ? (int)n0 : 0;
+      if (!uniform)
+        for (int64_t s = s0; s <= e; ++s) b->off[s - s0] = (int)(off[s] - off[s0]);
+      *first_stream = s0;
+      *first_row = off[s0];
+      return true;
+    }
+    return false;
+  }
+};
+
+void from_stream(CacheView& c, int64_t s) {
+  c.table += s * c.width;
+  c.lens += s;
+}
+
+logmel_status launched(int line) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? LOGMEL_OK : record_cuda_error(e, "kernel launch", "cache.cu", line);
+}
+
+}  // namespace
+
+extern "C" {
+
+logmel_status logmel_cache_rotary(const logmel_cache_config* config, double* inv_freq, double* length) {
+  if (!config || !inv_freq || !length) return LOGMEL_ERR_INVALID_ARG;
+  const logmel_status st = check_config(*config);
+  if (st != LOGMEL_OK) return st;
+  rotary_table(*config, inv_freq, length);
+  return LOGMEL_OK;
+}
+
+logmel_status logmel_cache_plan_create(const logmel_cache_config* config, logmel_cache_plan** out) {
+  if (!out) return LOGMEL_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!config) return LOGMEL_ERR_INVALID_ARG;
+  logmel_status st = check_config(*config);
+  if (st != LOGMEL_OK) return st;
+  logmel_cache_plan* p = new (std::nothrow) logmel_cache_plan();
+  if (!p) return LOGMEL_ERR_OOM;
+  p->cfg = *config;
+  while ((1 << p->page_shift) < config->page_size) ++p->page_shift;
+  p->group = config->n_q_heads / config->n_kv_heads;
+  p->scale = (float)(config->softmax_scale > 0.0 ? config->softmax_scale : 1.0 / std::sqrt((double)config->head_dim));
+  double inv[64], length;
+  rotary_table(*config, inv, &length);
+  for (int i = 0; i < config->rotary_dim / 2; ++i)   // long double holds 64 bits of mantissa; inv <= 1 radian
+    p->rotary.turn[i] = (uint64_t)((long double)inv[i] / (2.0L * 3.14159265358979323846264338327950288L) *
+                                                                 18446744073709551616.0L);
+  p->rotary.length = (float)length;
+  p->rotary.dim = config->rotary_dim;
+  auto fail = [&](logmel_status s) {
+    logmel_cache_plan_destroy(p);
+    return s;
+  };
+  cudaError_t e = cudaGetDevice(&p->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device);
+  if (e != cudaSuccess) return fail(record_cuda_error(e, "cudaDeviceGetAttribute", "cache.cu", __LINE__));
+  if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(LOGMEL_ERR_OOM);
+  }
+  if ((e = cudaMemset(p->d_status, 0, sizeof(int))) != cudaSuccess)
+    return fail(record_cuda_error(e, "cudaMemset", "cache.cu", __LINE__));
+  *out = p;
+  return LOGMEL_OK;
+}
+
+void logmel_cache_plan_destroy(logmel_cache_plan* p) {
+  if (!p) return;
+  if (p->d_status) {
+    DeviceScope dev(p->device);
+    cudaDeviceSynchronize();
+    cudaFree(p->d_status);
+  }
+  delete p;
+}
+
+logmel_status logmel_cache_append(logmel_cache_plan* p, const logmel_cache_view* cache, const int64_t* offsets,
+                                  const logmel_rows* q, const logmel_rows* k, const logmel_rows* v,
+                                  const int32_t* positions, const logmel_rows* q_out, void* stream) {
+  logmel_status st = check_view(p, cache);
+  int64_t rows = 0;
+  if (st == LOGMEL_OK) st = check_offsets(offsets, cache->n_streams, &rows);
+  if (st != LOGMEL_OK) return st;
+  const logmel_cache_config& c = p->cfg;
+  if ((st = check_rows(p, q, rows, c.n_q_heads, false)) != LOGMEL_OK) return st;
+  if ((st = check_rows(p, q_out, rows, c.n_q_heads, true)) != LOGMEL_OK) return st;
+  if ((st = check_rows(p, k, rows, c.n_kv_heads, false)) != LOGMEL_OK) return st;
+  if ((st = check_rows(p, v, rows, c.n_kv_heads, false)) != LOGMEL_OK) return st;
+  if (misaligned(positions, 4)) return LOGMEL_ERR_INVALID_ARG;
+  if (rows == 0) return LOGMEL_OK;
+  DeviceScope dev(p->device);
+  CK(dev.error());
+  AppendArgs a{};
+  a.n_q = c.n_q_heads;
+  a.n_kv = c.n_kv_heads;
+  a.head_dim = c.head_dim;
+  a.r = p->rotary;
+  Launches it{offsets, cache->n_streams};
+  int64_t s0, r0;
+  while (it.next(&a.b, &s0, &r0)) {
+    a.c = device_view(p, *cache);
+    from_stream(a.c, s0);
+    a.q = device_rows(*q, r0);
+    a.k = device_rows(*k, r0);
+    a.v = device_rows(*v, r0);
+    a.q_out = device_rows(*q_out, r0);
+    a.positions = positions ? positions + r0 : nullptr;
+    const cudaStream_t str = (cudaStream_t)stream;
+    if (c.dtype == LOGMEL_BF16) {
+      if (c.interleaved) append_kernel<__nv_bfloat16, true><<<a.b.rows, APPEND_THREADS, 0, str>>>(a);
+      else append_kernel<__nv_bfloat16, false><<<a.b.rows, APPEND_THREADS, 0, str>>>(a);
+    } else {
+      if (c.interleaved) append_kernel<__half, true><<<a.b.rows, APPEND_THREADS, 0, str>>>(a);
+      else append_kernel<__half, false><<<a.b.rows, APPEND_THREADS, 0, str>>>(a);
+    }
+    if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
+  }
+  return LOGMEL_OK;
+}
+
+logmel_status logmel_cache_attend(logmel_cache_plan* p, const logmel_cache_view* cache, const int64_t* offsets,
+                                  const logmel_rows* q, const logmel_rows* out, float* lse, int causal, int64_t window,
+                                  void* stream) {
+  logmel_status st = check_view(p, cache);
+  int64_t rows = 0;
+  if (st == LOGMEL_OK) st = check_offsets(offsets, cache->n_streams, &rows);
+  if (st != LOGMEL_OK) return st;
+  const logmel_cache_config& c = p->cfg;
+  if ((st = check_rows(p, q, rows, c.n_q_heads, false)) != LOGMEL_OK) return st;
+  if ((st = check_rows(p, out, rows, c.n_q_heads, true)) != LOGMEL_OK) return st;
+  if (window < 0 || misaligned(lse, 4)) return LOGMEL_ERR_INVALID_ARG;
+  if (rows == 0) return LOGMEL_OK;
+  if (q->data == out->data) return LOGMEL_ERR_INVALID_ARG;
+  DeviceScope dev(p->device);
+  CK(dev.error());
+  AttendArgs a{};
+  a.n_q = c.n_q_heads;
+  a.n_kv = c.n_kv_heads;
+  a.group = p->group;
+  a.causal = causal != 0;
+  a.window = (int)std::min<int64_t>(window, INT32_MAX / 2 + 1);   // wider than any length
+  a.scale = p->scale;
+  Launches it{offsets, cache->n_streams};
+  int64_t s0, r0;
+  while (it.next(&a.b, &s0, &r0)) {
+    a.c = device_view(p, *cache);
+    from_stream(a.c, s0);
+    a.q = device_rows(*q, r0);
+    a.out = device_rows(*out, r0);
+    a.lse = lse ? lse + r0 * c.n_q_heads : nullptr;
+    const cudaStream_t str = (cudaStream_t)stream;
+    const unsigned grid = (unsigned)(((int64_t)a.b.rows * c.n_q_heads + 3) / 4);
+    if (c.dtype == LOGMEL_BF16) {
+      if (c.head_dim == 128) attend_simple_kernel<__nv_bfloat16, 128><<<grid, 128, 0, str>>>(a);
+      else attend_simple_kernel<__nv_bfloat16, 64><<<grid, 128, 0, str>>>(a);
+    } else {
+      if (c.head_dim == 128) attend_simple_kernel<__half, 128><<<grid, 128, 0, str>>>(a);
+      else attend_simple_kernel<__half, 64><<<grid, 128, 0, str>>>(a);
+    }
+    if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
+  }
+  return LOGMEL_OK;
+}
+
+logmel_status logmel_cache_weigh(logmel_cache_plan* p, const logmel_cache_view* cache, const int64_t* offsets,
+                                 const logmel_rows* q, const float* lse, int causal, int64_t window, float decay,
+                                 float* mass_out, void* stream) {
+  logmel_status st = check_view(p, cache);
+  int64_t rows = 0;
+  if (st == LOGMEL_OK) st = check_offsets(offsets, cache->n_streams, &rows);
+  if (st != LOGMEL_OK) return st;
+  const logmel_cache_config& c = p->cfg;
+  if ((st = check_rows(p, q, rows, c.n_q_heads, false)) != LOGMEL_OK) return st;
+  if (window < 0 || !cache->mass || !mass_out || misaligned(mass_out, 16) || misaligned(lse, 4) || !std::isfinite(decay))
+    return LOGMEL_ERR_INVALID_ARG;
+  const int64_t mass_bytes = 4 * cache->n_pages * c.n_kv_heads * c.page_size;
+  if (mass_out != cache->mass && overlap(mass_out, mass_bytes, cache->mass, mass_bytes)) return LOGMEL_ERR_INVALID_ARG;
+  if (rows == 0) return LOGMEL_OK;
+  if (!lse) return LOGMEL_ERR_INVALID_ARG;
+  DeviceScope dev(p->device);
+  CK(dev.error());
+  WeighArgs a{};
+  a.n_q = c.n_q_heads;
+  a.n_kv = c.n_kv_heads;
+  a.group = p->group;
+  a.causal = causal != 0;
+  a.window = (int)std::min<int64_t>(window, INT32_MAX / 2 + 1);
+  a.scale = p->scale;
+  a.decay = decay;
+  a.out = mass_out;
+  Launches it{offsets, cache->n_streams};
+  int64_t s0, r0;
+  while (it.next(&a.b, &s0, &r0)) {
+    a.c = device_view(p, *cache);
+    from_stream(a.c, s0);
+    a.q = device_rows(*q, r0);
+    a.lse = lse + r0 * c.n_q_heads;
+    const cudaStream_t str = (cudaStream_t)stream;
+    const dim3 grid(64, c.n_kv_heads, a.b.streams);
+    if (c.dtype == LOGMEL_BF16) {
+      if (c.head_dim == 128) weigh_simple_kernel<__nv_bfloat16, 128><<<grid, 128, 0, str>>>(a);
+      else weigh_simple_kernel<__nv_bfloat16, 64><<<grid, 128, 0, str>>>(a);
+    } else {
+      if (c.head_dim == 128) weigh_simple_kernel<__half, 128><<<grid, 128, 0, str>>>(a);
+      else weigh_simple_kernel<__half, 64><<<grid, 128, 0, str>>>(a);
+    }
+    if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
+  }
+  return LOGMEL_OK;
+}
+
+logmel_status logmel_cache_evict(logmel_cache_plan* p, const logmel_cache_view* cache, const logmel_cache_view* to,
+                                 int64_t budget, int64_t recent, int32_t* kept, void* stream) {
+  logmel_status st = check_view(p, cache);
+  if (st == LOGMEL_OK) st = check_view(p, to);
+  if (st != LOGMEL_OK) return st;
+  const logmel_cache_config& c = p->cfg;
+  if (to->n_streams != cache->n_streams || !cache->mass || !to->mass || misaligned(kept, 4)) return LOGMEL_ERR_INVALID_ARG;
+  if (budget < 1 || recent < 0 || recent > budget || budget > (to->table_width << p->page_shift))
+    return LOGMEL_ERR_INVALID_ARG;
+  const int64_t streams = cache->n_streams;
+  if (streams == 0) return LOGMEL_OK;
+  if (!kept || overlap(cache->lens, 4 * streams, to->lens, 4 * streams)) return LOGMEL_ERR_INVALID_ARG;
+  if (budget > device_view(p, *to).capacity) return LOGMEL_ERR_INPUT_TOO_LONG;
+  DeviceScope dev(p->device);
+  CK(dev.error());
+  for (int64_t s0 = 0; s0 < streams; s0 += MAX_UNIFORM) {
+    const int n = (int)std::min<int64_t>(MAX_UNIFORM, streams - s0);
+    EvictArgs a{};
+    a.c = device_view(p, *cache);
+    a.to = device_view(p, *to);
+    from_stream(a.c, s0);
+    from_stream(a.to, s0);
+    a.n_kv = c.n_kv_heads;
+    a.head_dim = c.head_dim;
+    a.budget = (int)budget;
+    a.recent = (int)recent;
+    a.kept = kept + s0 * c.n_kv_heads * budget;
+    const cudaStream_t str = (cudaStream_t)stream;
+    select_kernel<<<dim3(c.n_kv_heads, n), SELECT_THREADS, 0, str>>>(a);
+    if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
+    gather_kernel<<<dim3((unsigned)((budget + GATHER_ROWS - 1) / GATHER_ROWS), c.n_kv_heads, n), GATHER_THREADS, 0, str>>>(a);
+    if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
+  }
+  return LOGMEL_OK;
+}
+
+logmel_status logmel_cache_device_status(logmel_cache_plan* p, int* code, void* stream) {
+  if (!p || !code) return LOGMEL_ERR_INVALID_ARG;
+  DeviceScope dev(p->device);
+  CK(dev.error());
+  const cudaStream_t str = (cudaStream_t)stream;
+  CK(cudaMemcpyAsync(code, p->d_status, sizeof(int), cudaMemcpyDeviceToHost, str));
+  CK(cudaMemsetAsync(p->d_status, 0, sizeof(int), str));
+  CK(cudaStreamSynchronize(str));
+  return LOGMEL_OK;
+}
+
+}  // extern "C"

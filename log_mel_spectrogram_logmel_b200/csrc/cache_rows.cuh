@@ -1,0 +1,267 @@
+// Token cache: the kernels that move rows (append, evict).  All of them are
+// bound by memory traffic; none computes more than a few operations a byte.
+#pragma once
+#include "cache_common.cuh"
+
+namespace logmel {
+namespace cache {
+
+// ---------------------------------------------------------------------------
+// append: rotary positions and the cache write
+// ---------------------------------------------------------------------------
+// Pair i of a head turns by position * f_i.  f_i is held as a fraction of a
+// turn in 64-bit fixed point (units of 2^-64 turns), so the product with an
+// integer position modulo 2^64 is the exact fraction of the turn, whatever
+// the position; its top 32 bits, read as a signed number of half turns, go to
+// sincospi.  An fp32 product position * f_i would be off by 4e-3 radians at
+// position 60,000.
+struct RotaryArgs {
+  uint64_t turn[64];   // per pair
+  float length;        // factor on a turned pair
+  int dim;             // turned dimensions
+};
+
+struct AppendArgs {
+  CacheView c;
+  Batch b;
+  Rows q, k, v, q_out;
+  const int* positions;
+  int n_q, n_kv, head_dim;
+  RotaryArgs r;
+};
+
+constexpr int APPEND_THREADS = 128;
+
+template <typename T>
+__device__ __forceinline__ uint4 turn_neighbours(uint4 x, const float2* cs, float) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 a = Half2<T>::to_float(w[j]);
+    w[j] = Half2<T>::from_float(a.x * cs[j].x - a.y * cs[j].y, a.y * cs[j].x + a.x * cs[j].y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ void turn_halves(uint4& lo, uint4& hi, const float2* cs) {
+  uint32_t* a = reinterpret_cast<uint32_t*>(&lo);
+  uint32_t* b = reinterpret_cast<uint32_t*>(&hi);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = Half2<T>::to_float(a[j]), y = Half2<T>::to_float(b[j]);
+    const float2 c0 = cs[2 * j], c1 = cs[2 * j + 1];
+    a[j] = Half2<T>::from_float(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
+    b[j] = Half2<T>::from_float(y.x * c0.x + x.x * c0.y, y.y * c1.x + x.y * c1.y);
+  }
+}
+
+// One CTA per new row.  A unit of work is 16 bytes (a pair of 16-byte pieces
+// where dimension i turns with i + dim / 2); the row's cosines and sines are
+// computed once and shared by all of its heads.
+template <typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ float2 cs[64];
+  __shared__ int dst[2];   // page (or -1) and slot in the page
+  const int t = blockIdx.x;
+  const int pairs = a.r.dim >> 1;
+  if (threadIdx.x < 64) {
+    const int s = a.b.stream_of(t);
+    const int n = a.b.count(s);
+    const int len = a.c.length(s, threadIdx.x == 0);
+    const int slot = len - n + (t - a.b.begin(s));
+    if (threadIdx.x < pairs) {
+      const int pos = a.positions ? a.positions[t] : slot;
+      const uint64_t phase = (uint64_t)(int64_t)pos * a.r.turn[threadIdx.x];
+      float sn, cn;
+      sincospif((float)(int)(phase >> 32) * 0x1p-31f, &sn, &cn);
+      cs[threadIdx.x] = make_float2(cn * a.r.length, sn * a.r.length);
+    }
+    if (threadIdx.x == 0) {
+      int page = -1;
+      if (slot >= 0) page = a.c.page(s, slot >> a.c.page_shift);   // slot < capacity: len is clamped
+      if (page < 0) a.c.flag();
+      dst[0] = page;
+      dst[1] = slot & ((1 << a.c.page_shift) - 1);
+    }
+  }
+  __syncthreads();
+  const int page = dst[0], slot = dst[1];
+  const int half = a.r.dim >> 4;                                   // 16-byte pieces of half the turned part
+  const int per_head = INTERLEAVED ? a.head_dim >> 3 : half + ((a.head_dim - a.r.dim) >> 3);
+  const int turned_units = (a.n_q + a.n_kv) * per_head;
+  const int plain = a.head_dim >> 3;
+  const int units = turned_units + a.n_kv * plain;
+  for (int u = threadIdx.x; u < units; u += APPEND_THREADS) {
+    if (u < turned_units) {
+      const int h = u / per_head, j = u - h * per_head;
+      const bool is_q = h < a.n_q;
+      const int hk = h - a.n_q;
+      if (!is_q && page < 0) continue;
+      const T* src = is_q ? (const T*)a.q.data + (int64_t)t * a.q.row + (int64_t)h * a.q.head
+                          : (const T*)a.k.data + (int64_t)t * a.k.row + (int64_t)hk * a.k.head;
+      T* out = is_q ? (T*)a.q_out.data + (int64_t)t * a.q_out.row + (int64_t)h * a.q_out.head
+                    : (T*)a.c.k + page * a.c.k_page + hk * a.c.k_head + slot * a.c.k_slot;
+      if (INTERLEAVED) {
+        uint4 x = *(const uint4*)(src + 8 * j);
+        if (8 * j < a.r.dim) x = turn_neighbours<T>(x, cs + 4 * j, 0.f);
+        *(uint4*)(out + 8 * j) = x;
+      } else if (j < half) {
+        uint4 lo = *(const uint4*)(src + 8 * j), hi = *(const uint4*)(src + 8 * (j + half));
+        turn_halves<T>(lo, hi, cs + 8 * j);
+        *(uint4*)(out + 8 * j) = lo;
+        *(uint4*)(out + 8 * (j + half)) = hi;
+      } else {
+        *(uint4*)(out + 8 * (j + half)) = *(const uint4*)(src + 8 * (j + half));
+      }
+    } else if (page >= 0) {
+      const int x = u - turned_units, h = x / plain, j = x - h * plain;
+      *(uint4*)((T*)a.c.v + page * a.c.v_page + h * a.c.v_head + slot * a.c.v_slot + 8 * j) =
+          *(const uint4*)((const T*)a.v.data + (int64_t)t * a.v.row + (int64_t)h * a.v.head + 8 * j);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// evict: keep the newest keys and those of largest weight, in other pages
+// ---------------------------------------------------------------------------
+struct EvictArgs {
+  CacheView c, to;
+  int n_kv, head_dim;
+  int budget, recent;
+  int* kept;   // [streams, n_kv, budget]
+};
+
+constexpr int SELECT_THREADS = 512;
+
+// Weights as unsigned keys of the same order: -0 as +0, NaN above all.
+__device__ __forceinline__ uint32_t rank_key(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t b = __float_as_uint(w + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float slot_mass(const EvictArgs& a, int s, int h, int j, bool& bad) {
+  const int p = a.c.page(s, j >> a.c.page_shift);
+  if (p < 0) {
+    bad = true;
+    return -INFINITY;
+  }
+  const int size = 1 << a.c.page_shift;
+  return a.c.mass[((int64_t)p * a.n_kv + h) * size + (j & (size - 1))];
+}
+
+// One CTA per stream and key head: the value of the k-th largest weight by a
+// radix selection (8 bits a pass), then one pass in slot order that writes
+// the kept slots.
+__global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const __grid_constant__ EvictArgs a) {
+  __shared__ int hist[256];
+  __shared__ int warp_sum[2][SELECT_THREADS / 32];
+  __shared__ uint32_t sh_prefix;
+  __shared__ int sh_need;
+  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int len = a.c.length(s, tid == 0);
+  const int m = min(len, a.budget);
+  const int old = len - min(len, a.recent);     // slots that compete
+  int need = len <= a.budget ? old : m - (len - old);
+  int* kept = a.kept + ((int64_t)s * a.n_kv + h) * a.budget;
+  bool bad = false;
+  uint32_t prefix = 0;
+  if (need < old && need > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int i = tid; i < 256; i += SELECT_THREADS) hist[i] = 0;
+      __syncthreads();
+      for (int j = tid; j < old; j += SELECT_THREADS) {
+        const uint32_t key = rank_key(slot_mass(a, s, h, j, bad));
+        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1);
+      }
+      __syncthreads();
+      if (tid == 0) {
+        int d = 255, left = need;
+        while (d > 0 && hist[d] < left) left -= hist[d--];
+        sh_prefix = prefix | ((uint32_t)d << shift);
+        sh_need = left;
+      }
+      __syncthreads();
+      prefix = sh_prefix;
+      need = sh_need;
+    }
+  }
+  // keys above `prefix` are kept, and of the equal ones the first `need`
+  const bool all = need >= old && len <= a.budget;
+  const bool none = !all && m - (len - old) == 0;
+  int above_before = 0, equal_before = 0;
+  for (int base = 0; base < old; base += SELECT_THREADS) {
+    const int j = base + tid;
+    bool gt = false, eq = false;
+    if (j < old && !none) {
+      if (all) gt = true;
+      else {
+        const uint32_t key = rank_key(slot_mass(a, s, h, j, bad));
+        gt = key > prefix;
+        eq = key == prefix;
+      }
+    }
+    const uint32_t bg = __ballot_sync(~0u, gt), be = __ballot_sync(~0u, eq);
+    if (lane == 0) {
+      warp_sum[0][warp] = __popc(bg);
+      warp_sum[1][warp] = __popc(be);
+    }
+    __syncthreads();
+    int g0 = above_before, e0 = equal_before, gt_all = 0, eq_all = 0;
+    for (int w = 0; w < SELECT_THREADS / 32; ++w) {
+      if (w < warp) {
+        g0 += warp_sum[0][w];
+        e0 += warp_sum[1][w];
+      }
+      gt_all += warp_sum[0][w];
+      eq_all += warp_sum[1][w];
+    }
+    const uint32_t below = (1u << lane) - 1;
+    g0 += __popc(bg & below);
+    e0 += __popc(be & below);
+    if (gt || (eq && e0 < need)) kept[g0 + min(e0, need)] = j;
+    above_before += gt_all;
+    equal_before += eq_all;
+    __syncthreads();
+  }
+  for (int i = tid; i < a.budget; i += SELECT_THREADS) {
+    if (i >= m) kept[i] = -1;
+    else if (i >= m - (len - old)) kept[i] = len - (m - i);
+  }
+  if (bad) a.c.flag();
+}
+
+constexpr int GATHER_ROWS = 32;
+constexpr int GATHER_THREADS = 256;
+
+// Copies the kept rows: one CTA per stream, key head and 32 kept rows; 16
+// bytes per thread and step.
+__global__ void __launch_bounds__(GATHER_THREADS) gather_kernel(const __grid_constant__ EvictArgs a) {
+  const int s = blockIdx.z, h = blockIdx.y, r0 = blockIdx.x * GATHER_ROWS;
+  const int len = a.c.length(s, false);
+  const int m = min(min(len, a.budget), a.to.capacity);
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.to.lens[s] = m;
+  if (r0 >= m) return;
+  const int per_row = a.head_dim >> 3, rows = min(GATHER_ROWS, m - r0), size = 1 << a.c.page_shift;
+  const int* kept = a.kept + ((int64_t)s * a.n_kv + h) * a.budget + r0;
+  for (int u = threadIdx.x; u < rows * per_row; u += GATHER_THREADS) {
+    const int r = u / per_row, x = (u - r * per_row) * 8;
+    const int from = kept[r], at = r0 + r;
+    const int p = a.c.page(s, from >> a.c.page_shift), q = a.to.page(s, at >> a.to.page_shift);
+    if (p < 0 || q < 0) {
+      a.c.flag();
+      continue;
+    }
+    const int f = from & (size - 1), d = at & (size - 1);
+    const uint4 k = *(const uint4*)((const uint16_t*)a.c.k + p * a.c.k_page + h * a.c.k_head + f * a.c.k_slot + x);
+    const uint4 v = *(const uint4*)((const uint16_t*)a.c.v + p * a.c.v_page + h * a.c.v_head + f * a.c.v_slot + x);
+    *(uint4*)((uint16_t*)a.to.k + q * a.to.k_page + h * a.to.k_head + d * a.to.k_slot + x) = k;
+    *(uint4*)((uint16_t*)a.to.v + q * a.to.v_page + h * a.to.v_head + d * a.to.v_slot + x) = v;
+    if (x == 0)
+      a.to.mass[((int64_t)q * a.n_kv + h) * size + d] = a.c.mass[((int64_t)p * a.n_kv + h) * size + f];
+  }
+}
+
+}  // namespace cache
+}  // namespace logmel

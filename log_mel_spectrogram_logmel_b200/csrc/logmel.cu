@@ -18,10 +18,23 @@
 #include <new>
 #include <vector>
 
+#include "internal.h"
 #include "logmel.h"
 #include "logmel_kernel.cuh"
 
 using namespace logmel;
+
+PFN_cuTensorMapEncodeTiled_v12000 logmel::tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    cudaGetLastError();
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+  }();
+  return fn;
+}
 
 namespace {
 
@@ -76,22 +89,6 @@ double hz_to_mel(double f) { return 2595.0 * std::log10(1.0 + f / 700.0); }
 double mel_to_hz(double m) { return 700.0 * (std::pow(10.0, m / 2595.0) - 1.0); }
 
 int64_t frames_of(int64_t n) { return n < NFFT ? 0 : (n - NFFT) / HOP + 1; }
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    cudaGetLastError();
-  }
-  return fn;
-}
 
 // Offline spans land as their even and their odd 160-sample hop blocks in
 // two regions, one box each: the tensor views below take every other row of
@@ -273,10 +270,14 @@ __global__ void carry_update_kernel(float* carry, int* carry_len, const float* c
 // Text of the last failed CUDA call on this host thread (logmel_last_error).
 static thread_local char g_last_error[256] = "";
 
-static logmel_status cuda_fail(cudaError_t e, const char* call, int line) {
-  snprintf(g_last_error, sizeof g_last_error, "%s: %s (%s, logmel.cu:%d)", cudaGetErrorName(e),
-           cudaGetErrorString(e), call, line);
+logmel_status logmel::record_cuda_error(cudaError_t e, const char* call, const char* file, int line) {
+  snprintf(g_last_error, sizeof g_last_error, "%s: %s (%s, %s:%d)", cudaGetErrorName(e), cudaGetErrorString(e), call,
+           file, line);
   return LOGMEL_ERR_CUDA;
+}
+
+static logmel_status cuda_fail(cudaError_t e, const char* call, int line) {
+  return record_cuda_error(e, call, "logmel.cu", line);
 }
 
 #define CK(call)                                           \
