@@ -24,6 +24,8 @@ struct logmel_cache_plan {
   float scale = 0.f;
   RotaryArgs rotary{};
   int* d_status = nullptr;
+  int* d_tickets = nullptr;   // split rows: one counter per worker, zero between calls
+  float* d_parts = nullptr;   // split rows: two partial tiles per worker
 };
 
 namespace {
@@ -185,6 +187,7 @@ Rows device_rows(const logmel_rows& r, int64_t first) {
 struct Launches {
   const int64_t* off;
   int64_t streams, at = 0;
+  int64_t most = 0;   // largest push of the current launch's streams
 
   bool next(Batch* b, int64_t* first_stream, int64_t* first_row) {
     while (at < streams) {
@@ -198,8 +201,12 @@ struct Launches {
       b->streams = (int)(e - s0);
       b->rows = (int)(off[e] - off[s0]);
       b->uniform = uniform ? (int)n0 : 0;
+      most = n0;
       if (!uniform)
-        for (int64_t s = s0; s <= e; ++s) b->off[s - s0] = (int)(off[s] - off[s0]);
+        for (int64_t s = s0; s <= e; ++s) {
+          b->off[s - s0] = (int)(off[s] - off[s0]);
+          if (s < e) most = std::max(most, off[s + 1] - off[s]);
+        }
       *first_stream = s0;
       *first_row = off[s0];
       return true;
@@ -211,6 +218,28 @@ struct Launches {
 void from_stream(CacheView& c, int64_t s) {
   c.table += s * c.width;
   c.lens += s;
+}
+
+// Bytes of the split kernels' partial tiles, whatever the lengths are.
+size_t parts_bytes(const logmel_cache_plan* p) {
+  const size_t rows = (size_t)2 * p->sms * ROWS_CTAS * ROWS_WARPS * sizeof(float) *
+                      (p->cfg.head_dim == 128 ? RowsShape<128>::PART : RowsShape<64>::PART);
+  return rows;
+}
+
+template <typename T, int D>
+cudaError_t allow_shared_memory() {
+  return cudaFuncSetAttribute(attend_rows_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsShape<D>::SMEM);
+}
+
+template <typename T, int D>
+void launch_attend(const logmel_cache_plan* p, const AttendArgs& a, int64_t most, cudaStream_t str) {
+  if (most * p->group <= ROWS_TILE) {
+    attend_rows_kernel<T, D><<<p->sms * ROWS_CTAS, ROWS_WARPS * 32, RowsShape<D>::SMEM, str>>>(a);
+  } else {
+    const unsigned grid = (unsigned)(((int64_t)a.b.rows * a.n_q + 3) / 4);
+    attend_simple_kernel<T, D><<<grid, 128, 0, str>>>(a);
+  }
 }
 
 logmel_status launched(int line) {
@@ -256,12 +285,20 @@ logmel_status logmel_cache_plan_create(const logmel_cache_config* config, logmel
   cudaError_t e = cudaGetDevice(&p->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device);
   if (e != cudaSuccess) return fail(record_cuda_error(e, "cudaDeviceGetAttribute", "cache.cu", __LINE__));
-  if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess) {
+  const size_t tickets = sizeof(int) * (size_t)p->sms * ROWS_CTAS * ROWS_WARPS;
+  if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess || cudaMalloc(&p->d_tickets, tickets) != cudaSuccess ||
+      cudaMalloc(&p->d_parts, parts_bytes(p)) != cudaSuccess) {
     cudaGetLastError();
     return fail(LOGMEL_ERR_OOM);
   }
-  if ((e = cudaMemset(p->d_status, 0, sizeof(int))) != cudaSuccess)
+  if ((e = cudaMemset(p->d_status, 0, sizeof(int))) != cudaSuccess ||
+      (e = cudaMemset(p->d_tickets, 0, tickets)) != cudaSuccess || (e = cudaDeviceSynchronize()) != cudaSuccess)
     return fail(record_cuda_error(e, "cudaMemset", "cache.cu", __LINE__));
+  if (config->dtype == LOGMEL_BF16)
+    e = config->head_dim == 128 ? allow_shared_memory<__nv_bfloat16, 128>() : allow_shared_memory<__nv_bfloat16, 64>();
+  else
+    e = config->head_dim == 128 ? allow_shared_memory<__half, 128>() : allow_shared_memory<__half, 64>();
+  if (e != cudaSuccess) return fail(record_cuda_error(e, "cudaFuncSetAttribute", "cache.cu", __LINE__));
   *out = p;
   return LOGMEL_OK;
 }
@@ -272,6 +309,8 @@ void logmel_cache_plan_destroy(logmel_cache_plan* p) {
     DeviceScope dev(p->device);
     cudaDeviceSynchronize();
     cudaFree(p->d_status);
+    cudaFree(p->d_tickets);
+    cudaFree(p->d_parts);
   }
   delete p;
 }
@@ -342,6 +381,8 @@ logmel_status logmel_cache_attend(logmel_cache_plan* p, const logmel_cache_view*
   a.causal = causal != 0;
   a.window = (int)std::min<int64_t>(window, INT32_MAX / 2 + 1);   // wider than any length
   a.scale = p->scale;
+  a.tickets = p->d_tickets;
+  a.parts = p->d_parts;
   Launches it{offsets, cache->n_streams};
   int64_t s0, r0;
   while (it.next(&a.b, &s0, &r0)) {
@@ -351,13 +392,12 @@ logmel_status logmel_cache_attend(logmel_cache_plan* p, const logmel_cache_view*
     a.out = device_rows(*out, r0);
     a.lse = lse ? lse + r0 * c.n_q_heads : nullptr;
     const cudaStream_t str = (cudaStream_t)stream;
-    const unsigned grid = (unsigned)(((int64_t)a.b.rows * c.n_q_heads + 3) / 4);
     if (c.dtype == LOGMEL_BF16) {
-      if (c.head_dim == 128) attend_simple_kernel<__nv_bfloat16, 128><<<grid, 128, 0, str>>>(a);
-      else attend_simple_kernel<__nv_bfloat16, 64><<<grid, 128, 0, str>>>(a);
+      if (c.head_dim == 128) launch_attend<__nv_bfloat16, 128>(p, a, it.most, str);
+      else launch_attend<__nv_bfloat16, 64>(p, a, it.most, str);
     } else {
-      if (c.head_dim == 128) attend_simple_kernel<__half, 128><<<grid, 128, 0, str>>>(a);
-      else attend_simple_kernel<__half, 64><<<grid, 128, 0, str>>>(a);
+      if (c.head_dim == 128) launch_attend<__half, 128>(p, a, it.most, str);
+      else launch_attend<__half, 64>(p, a, it.most, str);
     }
     if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
   }

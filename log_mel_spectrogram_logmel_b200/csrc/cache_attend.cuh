@@ -1,4 +1,8 @@
 // Token cache: attention of new rows over the cached slots.
+//
+// attend_rows_kernel serves pushes of few rows (new tokens x query heads of a
+// key head <= 16 in every stream), where every cached byte is used by a
+// handful of rows and memory traffic is the bound.
 #pragma once
 #include "cache_common.cuh"
 
@@ -13,7 +17,454 @@ struct AttendArgs {
   int n_q, n_kv, group;
   int causal, window;
   float scale;
+  int* tickets;        // one per worker, zero between calls
+  float* parts;        // split rows, two slots per worker
 };
+
+// ---------------------------------------------------------------------------
+// few rows
+// ---------------------------------------------------------------------------
+// The rows of one (stream, key head) fill one 16-row tensor-core tile; its
+// keys are cut into units of 16.  All units of the launch form one line,
+// (stream, key head, unit), which is cut into equal runs, one per warp: every
+// warp gets the same number of bytes whatever the lengths are, and no host
+// knowledge of the lengths is needed.  A warp copies its units through a ring
+// of its own with cp.async (no barrier with other warps; the ring runs ahead
+// across the borders of streams), so that 8 warps an SM keep about 130 KB in
+// flight.  Rows whose keys end up in several warps are joined by the last of
+// them to finish, in the order of the units, so results do not depend on timing.
+constexpr int ROWS_TILE = 16;
+constexpr int ROWS_WARPS = 4;
+constexpr int ROWS_CTAS = 2;                  // per SM
+constexpr int ROWS_MIN_UNITS = 4;             // a shorter run costs more in joining than it saves
+
+template <int D>
+struct RowsShape {
+  static constexpr int STAGES = D == 128 ? 3 : 6;
+  static constexpr int HALF = ROWS_TILE * D * 2;          // bytes of 16 keys
+  static constexpr int STAGE = 2 * HALF;                  // keys, then values
+  static constexpr int SMEM = ROWS_WARPS * STAGES * STAGE;
+  static constexpr int PART = ROWS_TILE * (D + 2);        // floats of a split tile: m, l, rows
+};
+
+__device__ __forceinline__ uint32_t smem_address(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
+  const int bytes = valid ? 16 : 0;   // the rest is filled with zeros
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Slots [lo, hi) that some new row of stream s sees, and the units of `step`
+// slots that cover them.  A stream with new rows has at least one unit, so
+// that rows that see nothing are still written.
+struct Extent {
+  int n, len, lo, hi, first, units;
+};
+
+__device__ __forceinline__ Extent extent_of(const AttendArgs& a, int s, int shift, bool report) {
+  Extent e;
+  e.n = a.b.count(s);
+  e.len = a.c.length(s, report);
+  e.lo = seen(e.len, e.n, 0, a.causal, a.window).x;
+  e.hi = e.len;
+  e.first = e.lo >> shift;
+  e.units = e.n == 0 ? 0 : max(1, ((e.hi + (1 << shift) - 1) >> shift) - e.first);
+  return e;
+}
+
+// A place on the line of units.
+struct Place {
+  int s, h, unit;    // unit counts from the item's first
+  Extent e;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel(const __grid_constant__ AttendArgs a) {
+  using Shape = RowsShape<D>;
+  constexpr int STAGES = Shape::STAGES, CHUNKS = D / 8, KSTEPS = D / 16, NT = D / 8;
+  constexpr float LOG2E = 1.4426950408889634f;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ int64_t before[ROWS_WARPS * 32 + 1];   // units (of one key head) before each thread's streams
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // the line: units of every stream, summed
+  const int per_thread = (a.b.streams + ROWS_WARPS * 32 - 1) / (ROWS_WARPS * 32);
+  {
+    int64_t sum = 0;
+    for (int i = 0; i < per_thread; ++i) {
+      const int s = tid * per_thread + i;
+      if (s < a.b.streams) sum += extent_of(a, s, 4, blockIdx.x == 0).units;
+    }
+    int64_t run = sum;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(~0u, run, d);
+      if (lane >= d) run += x;
+    }
+    if (lane == 31) before[warp * 32 + 32] = run;
+    __syncthreads();
+    int64_t base = 0;
+    for (int w = 0; w < warp; ++w) base += before[w * 32 + 32];
+    __syncthreads();
+    before[tid + 1] = base + run;
+    if (tid == 0) before[0] = 0;
+    __syncthreads();
+  }
+  const int64_t total = before[ROWS_WARPS * 32] * a.n_kv;
+  const int workers = gridDim.x * ROWS_WARPS, worker = blockIdx.x * ROWS_WARPS + warp;
+  const int64_t quota = max((int64_t)ROWS_MIN_UNITS, (total + workers - 1) / workers);
+  const int64_t u0 = worker * quota, u1 = min(total, u0 + quota);
+  if (u0 >= u1) return;
+
+  // the place of u0
+  Place at;
+  int64_t item_begin;   // first unit of the item at `at`
+  {
+    int lo = 0, hi = ROWS_WARPS * 32 - 1;   // last thread whose streams begin at or before u0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (before[mid] * a.n_kv <= u0) lo = mid;
+      else hi = mid - 1;
+    }
+    int64_t u = before[lo] * a.n_kv;
+    at.s = lo * per_thread;
+    for (;; ++at.s) {
+      at.e = extent_of(a, at.s, 4, false);
+      const int64_t here = (int64_t)at.e.units * a.n_kv;
+      if (u0 < u + here) break;
+      u += here;
+    }
+    at.h = (int)((u0 - u) / at.e.units);
+    at.unit = (int)(u0 - u - (int64_t)at.h * at.e.units);
+    item_begin = u0 - at.unit;
+  }
+  auto step = [&](Place& p) {   // to the next unit of the line (which exists)
+    if (++p.unit < p.e.units) return;
+    p.unit = 0;
+    if (++p.h < a.n_kv) return;
+    p.h = 0;
+    do p.e = extent_of(a, ++p.s, 4, false);
+    while (p.e.units == 0);
+  };
+  auto page_of = [&](const Place& p) {
+    const int key = (p.e.first + p.unit) << 4;
+    if (key >= p.e.hi) return -2;   // the one unit of rows that see nothing
+    return a.c.page(p.s, key >> a.c.page_shift);
+  };
+
+  // ring
+  const uint32_t ring = smem_address(smem) + warp * STAGES * Shape::STAGE;
+  constexpr int ROWS_PER_STEP = 32 / CHUNKS, STEPS = ROWS_TILE / ROWS_PER_STEP;
+  const int my_row = lane / CHUNKS, my_chunk = lane % CHUNKS;
+  const int in_page = (1 << a.c.page_shift) - 1;
+  auto issue = [&](const Place& p, int page, int stage) {
+    const int key = (p.e.first + p.unit) << 4;
+    if (page == -1 && lane == 0) a.c.flag();
+    const char* k = a.c.k;
+    const char* v = a.c.v;
+    const int at0 = key & in_page;
+    if (page >= 0) {
+      k += 2 * ((int64_t)page * a.c.k_page + p.h * a.c.k_head + (at0 + my_row) * a.c.k_slot + 8 * my_chunk);
+      v += 2 * ((int64_t)page * a.c.v_page + p.h * a.c.v_head + (at0 + my_row) * a.c.v_slot + 8 * my_chunk);
+    }
+    const uint32_t dst = ring + stage * Shape::STAGE;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int r = my_row + i * ROWS_PER_STEP;
+      const bool live = page >= 0 && key + r >= p.e.lo && key + r < p.e.hi;
+      const uint32_t off = r * (D * 2) + ((my_chunk ^ (r & 7)) << 4);
+      copy16(dst + off, live ? k + (int64_t)i * ROWS_PER_STEP * 2 * a.c.k_slot : a.c.k, live);
+      copy16(dst + Shape::HALF + off, live ? v + (int64_t)i * ROWS_PER_STEP * 2 * a.c.v_slot : a.c.v, live);
+    }
+  };
+  Place ahead = at;
+  int64_t ahead_u = u0;
+  int ahead_page = page_of(ahead);
+  auto produce = [&](int stage) {
+    if (ahead_u < u1) {
+      issue(ahead, ahead_page, stage);
+      if (++ahead_u < u1) {
+        step(ahead);
+        ahead_page = page_of(ahead);   // read one unit early: its latency hides behind this unit
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) produce(i);
+
+  const float sc = a.scale * LOG2E;
+  const int gr = lane >> 2, gc = lane & 3;
+  uint32_t q[KSTEPS][4];
+  float o[NT][4], m[2], l[2];
+  int2 row_seen[2];
+  int rows = 0;
+  bool mixed_rows = false;
+  int2 all_see = make_int2(0, 0);
+  const T* qrow[2];
+
+  auto begin_item = [&] {
+    rows = at.e.n * a.group;
+    const int64_t t0 = a.b.begin(at.s);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = gr + 8 * i;
+      const bool valid = r < rows;
+      const int tok = valid ? r / a.group : 0;
+      qrow[i] = (const T*)a.q.data + (t0 + tok) * a.q.row + (int64_t)(at.h * a.group + r - tok * a.group) * a.q.head;
+      row_seen[i] = valid ? seen(at.e.len, at.e.n, tok, a.causal, a.window) : make_int2(0, 0);
+#pragma unroll
+      for (int j = 0; j < KSTEPS; ++j) {
+        q[j][i] = valid ? *(const uint32_t*)(qrow[i] + 16 * j + 2 * gc) : 0u;
+        q[j][i + 2] = valid ? *(const uint32_t*)(qrow[i] + 16 * j + 8 + 2 * gc) : 0u;
+      }
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+    const int2 first = seen(at.e.len, at.e.n, 0, a.causal, a.window);
+    const int2 last = seen(at.e.len, at.e.n, at.e.n - 1, a.causal, a.window);
+    all_see = make_int2(last.x, first.y);   // seen by every row
+    mixed_rows = at.e.n > 1;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+  };
+  begin_item();
+  bool from_start = at.unit == 0;
+
+  int stage = 0;
+  for (int64_t u = u0; u < u1; ++u) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    __syncwarp();
+    produce(stage == 0 ? STAGES - 1 : stage - 1);   // the stage that the previous unit left
+    const uint32_t ks = ring + stage * Shape::STAGE, vs = ks + Shape::HALF;
+    const int key = (at.e.first + at.unit) << 4;
+
+    // scores of 16 rows x 16 keys
+    float x[2][4] = {};
+#pragma unroll
+    for (int j = 0; j < KSTEPS; ++j) {
+      uint32_t b[4];
+      const int r = (lane & 7) + ((lane & 16) >> 1), c = 2 * j + ((lane >> 3) & 1);
+      ldmatrix4(b, ks + r * (D * 2) + ((c ^ (r & 7)) << 4));
+      mma16816<T>(x[0], q[j], b[0], b[1]);
+      mma16816<T>(x[1], q[j], b[2], b[3]);
+    }
+    const bool edge = key < all_see.x || key + 16 > all_see.y;
+    if (edge) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = key + 8 * t + 2 * gc + (e & 1), i = e >> 1;
+          if (j < row_seen[i].x || j >= row_seen[i].y) x[t][e] = -INFINITY;
+        }
+    }
+    float top[2], use[2];
+    bool grew = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float t = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
+      t = fmaxf(t, __shfl_xor_sync(~0u, t, 1));
+      t = fmaxf(t, __shfl_xor_sync(~0u, t, 2));
+      top[i] = fmaxf(m[i], t * sc);
+      grew |= top[i] > m[i];
+    }
+    if (__any_sync(~0u, grew)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float f = top[i] > m[i] ? exp2_approx(m[i] - top[i]) : 1.f;   // 0 when m is minus infinity
+        m[i] = top[i];
+        l[i] *= f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          o[j][2 * i] *= f;
+          o[j][2 * i + 1] *= f;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) use[i] = m[i] == -INFINITY ? 0.f : m[i];
+    uint32_t p[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float p0 = exp2_approx(fmaf(x[t][2 * i], sc, -use[i])), p1 = exp2_approx(fmaf(x[t][2 * i + 1], sc, -use[i]));
+        l[i] += p0 + p1;                                        // summed before the weights are rounded
+        p[2 * t + i] = Half2<T>::from_float(p0, p1);
+      }
+    // Values that are not finite may only reach the rows that see them, and
+    // 0 x inf is not 0: where rows differ in what they see, look first.
+    bool apart = false;
+    if (edge && mixed_rows) {
+      bool bad = false;
+      for (int i = lane; i < ROWS_TILE * CHUNKS; i += 32) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(vs + 16 * i));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          constexpr uint32_t E = Half2<T>::EXPONENT;
+          bad |= (w[e] & E & 0xffffu) == (E & 0xffffu) || (w[e] & E & 0xffff0000u) == (E & 0xffff0000u);
+        }
+      }
+      apart = __any_sync(~0u, bad);
+    }
+    const int vr = (lane & 7) + (lane & 8), vc = lane >> 4;
+    if (!apart) {
+#pragma unroll
+      for (int j = 0; j < NT / 2; ++j) {
+        uint32_t b[4];
+        ldmatrix4_trans(b, vs + vr * (D * 2) + (((2 * j + vc) ^ (vr & 7)) << 4));
+        mma16816<T>(o[2 * j], p, b[0], b[1]);
+        mma16816<T>(o[2 * j + 1], p, b[2], b[3]);
+      }
+    } else {
+      for (int e = 0; e < 16; ++e) {   // one key at a time, added only to the rows that see it
+        const uint32_t mine = (e >> 1 & 3) == gc ? (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
+        const uint32_t lo = e < 8 ? mine : 0u, hi = e < 8 ? 0u : mine;
+        const uint32_t pe[4] = {p[0] & lo, p[1] & lo, p[2] & hi, p[3] & hi};
+        bool sees[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sees[i] = key + e >= row_seen[i].x && key + e < row_seen[i].y;
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, vs + vr * (D * 2) + (((2 * j + vc) ^ (vr & 7)) << 4));
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            float y[4] = {};
+            mma16816<T>(y, pe, b[2 * t] & lo, b[2 * t + 1] & hi);
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (sees[w >> 1]) o[2 * j + t][w] += y[w];
+          }
+        }
+      }
+    }
+    if (++stage == STAGES) stage = 0;
+
+    const bool item_done = at.unit + 1 == at.e.units;
+    if (!item_done && u + 1 < u1) {
+      ++at.unit;
+      continue;
+    }
+    // the end of the item, or of this warp's run
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(~0u, l[i], 1);
+      l[i] += __shfl_xor_sync(~0u, l[i], 2);
+    }
+    const int64_t t0 = a.b.begin(at.s);
+    if (item_done && from_start) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = gr + 8 * i;
+        if (r >= rows) continue;
+        const int tok = r / a.group, hq = at.h * a.group + r - tok * a.group;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        T* out = (T*)a.out.data + (t0 + tok) * a.out.row + (int64_t)hq * a.out.head;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          *(uint32_t*)(out + 8 * j + 2 * gc) = l[i] == 0.f ? 0u : Half2<T>::from_float(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
+        if (a.lse && gc == 0) a.lse[(t0 + tok) * a.n_q + hq] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+      }
+    } else {
+      // slot 0: an item that began before this run; slot 1: one that began in it
+      float* part = a.parts + (int64_t)(2 * worker + (from_start ? 1 : 0)) * Shape::PART;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = gr + 8 * i;
+        if (r >= rows) continue;
+        if (gc == 0) {
+          __stcg(part + r, m[i]);
+          __stcg(part + ROWS_TILE + r, l[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          __stcg((float2*)(part + 2 * ROWS_TILE + r * D + 8 * j + 2 * gc), make_float2(o[j][2 * i], o[j][2 * i + 1]));
+      }
+      __threadfence();
+      __syncwarp();
+      const int first = (int)(item_begin / quota), last = (int)((item_begin + at.e.units - 1) / quota);
+      int done = 0;
+      if (lane == 0) done = atomicAdd(a.tickets + first, 1);
+      done = __shfl_sync(~0u, done, 0);
+      if (done == last - first) {
+        if (lane == 0) a.tickets[first] = 0;   // ready for the next call
+        __threadfence();
+        auto slot = [&](int w) { return a.parts + (int64_t)(2 * w + (w == first ? 1 : 0)) * Shape::PART; };
+        for (int r = 0; r < rows; ++r) {
+          float mm = -INFINITY;
+          for (int w = first + lane; w <= last; w += 32) mm = fmaxf(mm, __ldcg(slot(w) + r));
+          for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
+          const float base = mm == -INFINITY ? 0.f : mm;
+          constexpr int V = D / 32;
+          float acc[V] = {}, sum = 0.f;
+#pragma unroll 8
+          for (int w = first; w <= last; ++w) {
+            const float* s = slot(w);
+            const float f = exp2_approx(__ldcg(s + r) - base);
+            sum += f * __ldcg(s + ROWS_TILE + r);
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              const float2 y = __ldcg((const float2*)(s + 2 * ROWS_TILE + r * D + V * lane + e));
+              acc[e] += f * y.x;
+              acc[e + 1] += f * y.y;
+            }
+          }
+          const int tok = r / a.group, hq = at.h * a.group + r - tok * a.group;
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          T* out = (T*)a.out.data + (t0 + tok) * a.out.row + (int64_t)hq * a.out.head;
+#pragma unroll
+          for (int e = 0; e < V; e += 2)
+            *(uint32_t*)(out + V * lane + e) = sum == 0.f ? 0u : Half2<T>::from_float(acc[e] * inv, acc[e + 1] * inv);
+          if (a.lse && lane == 0) a.lse[(t0 + tok) * a.n_q + hq] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * 0.6931471805599453f;
+        }
+      }
+    }
+    if (u + 1 < u1) {
+      step(at);
+      item_begin = u + 1;
+      from_start = true;
+      begin_item();
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
+// many rows
+// ---------------------------------------------------------------------------
 
 // One warp per new row and query head: the lanes hold the head's dimensions,
 // keys are taken one by one with a running maximum and sum.
