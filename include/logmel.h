@@ -387,7 +387,7 @@ logmel_status logmel_partition_streams(int64_t n_streams, int n_parts, int64_t* 
  *   - Rows are 16-bit floats of the plan's type.  Row arrays may be strided
  *     (slices of a fused projection): element (t, h, d) of a logmel_rows lies
  *     at data + t * row_stride + h * head_stride + d.  Base addresses must be
- *     16-byte aligned and strides non-negative multiples of 8 elements; rows
+ *     16-byte aligned and strides positive multiples of 8 elements; rows
  *     and pages that are written must not overlap one another; else
  *     LOGMEL_ERR_INVALID_ARG.  Sums, softmax statistics and weights are fp32.
  *   - A page id outside 0 .. n_pages - 1, a length that the table cannot hold

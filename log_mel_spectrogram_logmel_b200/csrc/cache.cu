@@ -9,6 +9,7 @@
 #include <new>
 
 #include "cache_attend.cuh"
+#include "cache_chunk.cuh"
 #include "cache_common.cuh"
 #include "cache_rows.cuh"
 #include "cache_weigh.cuh"
@@ -119,7 +120,7 @@ bool distinct(int64_t d, int dims, const int64_t* size, const int64_t* stride) {
 
 logmel_status check_rows(const logmel_cache_plan* p, const logmel_rows* r, int64_t rows, int heads, bool output) {
   if (!r) return LOGMEL_ERR_INVALID_ARG;
-  if (r->row_stride < 0 || r->head_stride < 0 || r->row_stride % 8 || r->head_stride % 8) return LOGMEL_ERR_INVALID_ARG;
+  if (r->row_stride < 8 || r->head_stride < 8 || r->row_stride % 8 || r->head_stride % 8) return LOGMEL_ERR_INVALID_ARG;
   if (rows == 0) return LOGMEL_OK;
   if (!r->data || misaligned(r->data, 16)) return LOGMEL_ERR_INVALID_ARG;
   // products of sizes and strides stay far inside 64 bits
@@ -222,29 +223,74 @@ void from_stream(CacheView& c, int64_t s) {
 
 // Bytes of the split kernels' partial tiles, whatever the lengths are.
 size_t parts_bytes(const logmel_cache_plan* p) {
-  const size_t rows = (size_t)2 * p->sms * ROWS_CTAS * ROWS_WARPS * sizeof(float) *
-                      (p->cfg.head_dim == 128 ? RowsShape<128>::PART : RowsShape<64>::PART);
-  return rows;
+  const bool wide = p->cfg.head_dim == 128;
+  const size_t rows = (size_t)ROWS_CTAS * ROWS_WARPS * (wide ? RowsShape<128>::PART : RowsShape<64>::PART);
+  const size_t chunk = wide ? ChunkShape<128>::PART : ChunkShape<64>::PART;
+  return std::max(rows, chunk) * 2 * p->sms * sizeof(float);
 }
 
 template <typename T, int D>
 cudaError_t allow_shared_memory() {
-  return cudaFuncSetAttribute(attend_rows_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsShape<D>::SMEM);
+  const cudaError_t e =
+      cudaFuncSetAttribute(attend_rows_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsShape<D>::SMEM);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(attend_chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 ChunkShape<D>::SMEM);
 }
 
-template <typename T, int D>
-void launch_attend(const logmel_cache_plan* p, const AttendArgs& a, int64_t most, cudaStream_t str) {
-  if (most * p->group <= ROWS_TILE) {
-    attend_rows_kernel<T, D><<<p->sms * ROWS_CTAS, ROWS_WARPS * 32, RowsShape<D>::SMEM, str>>>(a);
-  } else {
-    const unsigned grid = (unsigned)(((int64_t)a.b.rows * a.n_q + 3) / 4);
-    attend_simple_kernel<T, D><<<grid, 128, 0, str>>>(a);
-  }
+CUtensorMapDataType element_type(const logmel_cache_plan* p) {
+  return p->cfg.dtype == LOGMEL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+// Query rows as a tensor [row][head][d]; a box is 64 columns of the key
+// head's query heads, for the tokens of a tile.
+bool encode_rows(const logmel_cache_plan* p, CUtensorMap* m, const Rows& r, int rows, int heads, int tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)p->cfg.head_dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {2 * (cuuint64_t)r.head, 2 * (cuuint64_t)r.row};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p->group, (cuuint32_t)tokens}, one[3] = {1, 1, 1};
+  return tensor_map_encoder()(m, element_type(p), 3, r.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pages as a tensor [page][head][slot][d]; a box is 64 columns of `slots` slots of one page.
+bool encode_pages(const logmel_cache_plan* p, CUtensorMap* m, char* base, int64_t n_pages, int64_t page, int64_t head,
+                  int64_t slot, int slots) {
+  const cuuint64_t dims[4] = {(cuuint64_t)p->cfg.head_dim, (cuuint64_t)p->cfg.page_size, (cuuint64_t)p->cfg.n_kv_heads,
+                              (cuuint64_t)n_pages};
+  const cuuint64_t strides[3] = {2 * (cuuint64_t)slot, 2 * (cuuint64_t)head, 2 * (cuuint64_t)page};
+  const cuuint32_t box[4] = {64, (cuuint32_t)slots, 1, 1}, one[4] = {1, 1, 1, 1};
+  return tensor_map_encoder()(m, element_type(p), 4, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+logmel_status no_map(int line) {
+  return record_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled", "cache.cu", line);
 }
 
 logmel_status launched(int line) {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? LOGMEL_OK : record_cuda_error(e, "kernel launch", "cache.cu", line);
+}
+
+template <typename T, int D>
+logmel_status launch_attend(const logmel_cache_plan* p, const AttendArgs& a, int64_t most, cudaStream_t str) {
+  if (most * p->group <= ROWS_TILE) {
+    attend_rows_kernel<T, D><<<p->sms * ROWS_CTAS, ROWS_WARPS * 32, RowsShape<D>::SMEM, str>>>(a);
+  } else {
+    ChunkArgs x;
+    static_cast<AttendArgs&>(x) = a;
+    x.tokens = TILE_ROWS / p->group;
+    x.box_keys = std::min(p->cfg.page_size, TILE_KEYS);
+    const CacheView& c = a.c;
+    if (!encode_rows(p, &x.q_map, a.q, a.b.rows, a.n_q, x.tokens) ||
+        !encode_pages(p, &x.k_map, c.k, c.n_pages, c.k_page, c.k_head, c.k_slot, x.box_keys) ||
+        !encode_pages(p, &x.v_map, c.v, c.n_pages, c.v_page, c.v_head, c.v_slot, x.box_keys))
+      return no_map(__LINE__);
+    attend_chunk_kernel<T, D><<<p->sms, CHUNK_THREADS, ChunkShape<D>::SMEM, str>>>(x);
+  }
+  return launched(__LINE__);
 }
 
 }  // namespace
@@ -285,6 +331,7 @@ logmel_status logmel_cache_plan_create(const logmel_cache_config* config, logmel
   cudaError_t e = cudaGetDevice(&p->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device);
   if (e != cudaSuccess) return fail(record_cuda_error(e, "cudaDeviceGetAttribute", "cache.cu", __LINE__));
+  if (!tensor_map_encoder()) return fail(record_cuda_error(cudaErrorNotSupported, "cuTensorMapEncodeTiled", "cache.cu", __LINE__));
   const size_t tickets = sizeof(int) * (size_t)p->sms * ROWS_CTAS * ROWS_WARPS;
   if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess || cudaMalloc(&p->d_tickets, tickets) != cudaSuccess ||
       cudaMalloc(&p->d_parts, parts_bytes(p)) != cudaSuccess) {
@@ -393,13 +440,12 @@ logmel_status logmel_cache_attend(logmel_cache_plan* p, const logmel_cache_view*
     a.lse = lse ? lse + r0 * c.n_q_heads : nullptr;
     const cudaStream_t str = (cudaStream_t)stream;
     if (c.dtype == LOGMEL_BF16) {
-      if (c.head_dim == 128) launch_attend<__nv_bfloat16, 128>(p, a, it.most, str);
-      else launch_attend<__nv_bfloat16, 64>(p, a, it.most, str);
+      st = c.head_dim == 128 ? launch_attend<__nv_bfloat16, 128>(p, a, it.most, str)
+                             : launch_attend<__nv_bfloat16, 64>(p, a, it.most, str);
     } else {
-      if (c.head_dim == 128) launch_attend<__half, 128>(p, a, it.most, str);
-      else launch_attend<__half, 64>(p, a, it.most, str);
+      st = c.head_dim == 128 ? launch_attend<__half, 128>(p, a, it.most, str) : launch_attend<__half, 64>(p, a, it.most, str);
     }
-    if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
+    if (st != LOGMEL_OK) return st;
   }
   return LOGMEL_OK;
 }

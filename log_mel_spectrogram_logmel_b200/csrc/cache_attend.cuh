@@ -4,7 +4,7 @@
 // key head <= 16 in every stream), where every cached byte is used by a
 // handful of rows and memory traffic is the bound.
 #pragma once
-#include "cache_common.cuh"
+#include "cache_tensor.cuh"
 
 namespace logmel {
 namespace cache {
@@ -47,8 +47,6 @@ struct RowsShape {
   static constexpr int PART = ROWS_TILE * (D + 2);        // floats of a split tile: m, l, rows
 };
 
-__device__ __forceinline__ uint32_t smem_address(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
   const int bytes = valid ? 16 : 0;   // the rest is filled with zeros
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -79,12 +77,6 @@ __device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, ui
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Slots [lo, hi) that some new row of stream s sees, and the units of `step`
 // slots that cover them.  A stream with new rows has at least one unit, so
 // that rows that see nothing are still written.
@@ -113,7 +105,6 @@ template <typename T, int D>
 __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel(const __grid_constant__ AttendArgs a) {
   using Shape = RowsShape<D>;
   constexpr int STAGES = Shape::STAGES, CHUNKS = D / 8, KSTEPS = D / 16, NT = D / 8;
-  constexpr float LOG2E = 1.4426950408889634f;
   extern __shared__ __align__(128) char smem[];
   __shared__ int64_t before[ROWS_WARPS * 32 + 1];   // units (of one key head) before each thread's streams
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -396,7 +387,7 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
 #pragma unroll
         for (int j = 0; j < NT; ++j)
           *(uint32_t*)(out + 8 * j + 2 * gc) = l[i] == 0.f ? 0u : Half2<T>::from_float(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
-        if (a.lse && gc == 0) a.lse[(t0 + tok) * a.n_q + hq] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+        if (a.lse && gc == 0) a.lse[(t0 + tok) * a.n_q + hq] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * LN2;
       }
     } else {
       // slot 0: an item that began before this run; slot 1: one that began in it
@@ -448,7 +439,7 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
 #pragma unroll
           for (int e = 0; e < V; e += 2)
             *(uint32_t*)(out + V * lane + e) = sum == 0.f ? 0u : Half2<T>::from_float(acc[e] * inv, acc[e + 1] * inv);
-          if (a.lse && lane == 0) a.lse[(t0 + tok) * a.n_q + hq] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * 0.6931471805599453f;
+          if (a.lse && lane == 0) a.lse[(t0 + tok) * a.n_q + hq] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * LN2;
         }
       }
     }
@@ -460,65 +451,6 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-// ---------------------------------------------------------------------------
-// many rows
-// ---------------------------------------------------------------------------
-
-// One warp per new row and query head: the lanes hold the head's dimensions,
-// keys are taken one by one with a running maximum and sum.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) attend_simple_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int P = D / 64;   // 2-element pieces per lane
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (w >= (int64_t)a.b.rows * a.n_q) return;
-  const int t = (int)(w / a.n_q), h = (int)(w - (int64_t)t * a.n_q), hk = h / a.group;
-  const int s = a.b.stream_of(t), n = a.b.count(s);
-  const int len = a.c.length(s, lane == 0);
-  const int2 r = seen(len, n, t - a.b.begin(s), a.causal, a.window);
-  float2 q[P], o[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    q[i] = Half2<T>::to_float(
-        *(const uint32_t*)((const T*)a.q.data + (int64_t)t * a.q.row + (int64_t)h * a.q.head + 64 * i + 2 * lane));
-    o[i] = make_float2(0.f, 0.f);
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = r.x; j < r.y; ++j) {
-    const int p = a.c.page(s, j >> a.c.page_shift), x = j & ((1 << a.c.page_shift) - 1);
-    if (p < 0) {
-      a.c.flag();
-      continue;
-    }
-    const T* k = (const T*)a.c.k + p * a.c.k_page + hk * a.c.k_head + x * a.c.k_slot;
-    const T* v = (const T*)a.c.v + p * a.c.v_page + hk * a.c.v_head + x * a.c.v_slot;
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const float2 y = Half2<T>::to_float(*(const uint32_t*)(k + 64 * i + 2 * lane));
-      dot += q[i].x * y.x + q[i].y * y.y;
-    }
-    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(~0u, dot, d);
-    dot *= a.scale;
-    const float top = fmaxf(m, dot);
-    const float c = top == -INFINITY ? 1.f : expf(m - top), e = top == -INFINITY ? 0.f : expf(dot - top);
-    l = l * c + e;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const float2 y = Half2<T>::to_float(*(const uint32_t*)(v + 64 * i + 2 * lane));
-      o[i].x = o[i].x * c + e * y.x;
-      o[i].y = o[i].y * c + e * y.y;
-    }
-    m = top;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int i = 0; i < P; ++i)
-    *(uint32_t*)((T*)a.out.data + (int64_t)t * a.out.row + (int64_t)h * a.out.head + 64 * i + 2 * lane) =
-        Half2<T>::from_float(o[i].x * inv, o[i].y * inv);
-  if (a.lse && lane == 0) a.lse[(int64_t)t * a.n_q + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 }  // namespace cache

@@ -1,0 +1,621 @@
+// Token cache: attention of many new rows over the cached slots (tcgen05).
+//
+// An item is 256 rows of one (stream, key head): two 128-row tiles of tokens x
+// query heads of the key head, so that heads which share keys share the loads.  Keys
+// come in units of 128 slots.  All units of the launch form one line (stream,
+// key head, item, unit) that is cut into equal runs, one per CTA; items that
+// fall into several runs are joined by the CTA that finishes last, in order.
+//
+// Roles of a CTA (384 threads):
+//   warps 0-3, 4-7   softmax of tile 0 and of tile 1, one thread per row: scores from
+//                    tensor memory, running maximum and sum in registers, weights back to
+//                    tensor memory as the left operand of the product with the values
+//   warp 8           TMA: queries of an item, then keys and values by page
+//   warp 9           issues the MMAs; the two tiles alternate, so that one tile's
+//                    softmax runs under the other's products
+//   warps 10, 11     clean values: slots that no row of the item sees are zeroed (0 x NaN
+//                    is not 0), and where rows differ in what they see, values that are not
+//                    finite are taken out and added to the rows that see them at the end
+//
+// The accumulator is rescaled only when a row's maximum has grown by more
+// than 2^8 since the last time; weights stay below 2^8 and the sum is exact either way.
+#pragma once
+#include "cache_attend.cuh"
+
+namespace logmel {
+namespace cache {
+
+constexpr int TILE_ROWS = 128;
+constexpr int ITEM_ROWS = 2 * TILE_ROWS;
+constexpr int TILE_KEYS = 128;
+constexpr int CHUNK_THREADS = 384;
+constexpr int CHUNK_MIN_UNITS = 2;
+constexpr float RESCALE_AT = 8.f;   // in powers of two
+
+template <int D>
+struct ChunkShape {
+  static constexpr int TILE = TILE_ROWS * D * 2;              // bytes of 128 rows
+  static constexpr int STAGES = D == 128 ? 5 : 8;             // tiles of keys or values in the ring
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE;
+  static constexpr int PART = ITEM_ROWS * (D + 2);            // floats of a split item: m, l, then [D / 4][row][4]
+  static constexpr int O_COLUMN = 256;                        // accumulators at 256 and 384, scores at 0 and 128
+};
+
+struct ChunkArgs : AttendArgs {
+  CUtensorMap q_map, k_map, v_map;
+  int tokens;      // tokens of a tile: 128 / group
+  int box_keys;    // slots a key copy brings: min(page size, 128)
+};
+
+// Item `qt` of a stream: its tokens, the slots its rows see, the units that cover them.
+struct Item {
+  int i0, count;          // tokens
+  int lo, hi;             // seen by some row
+  int2 first, last;       // seen by the first and by the last token
+  int begin, units;       // in units of 128 slots
+};
+
+__device__ __forceinline__ Item item_of(const ChunkArgs& a, int n, int len, int qt) {
+  Item x;
+  x.i0 = qt * 2 * a.tokens;
+  x.count = min(2 * a.tokens, n - x.i0);
+  x.first = seen(len, n, x.i0, a.causal, a.window);
+  x.last = seen(len, n, x.i0 + x.count - 1, a.causal, a.window);
+  x.lo = x.first.x;
+  x.hi = x.last.y;
+  x.begin = x.lo / TILE_KEYS;
+  x.units = max(1, (x.hi + TILE_KEYS - 1) / TILE_KEYS - x.begin);
+  return x;
+}
+
+struct ChunkPlace {
+  int s, h, qt, unit;
+  int n, len, items;
+  Item x;
+
+  __device__ void load_stream(const ChunkArgs& a) {
+    n = a.b.count(s);
+    len = a.c.length(s, false);
+    items = (n + 2 * a.tokens - 1) / (2 * a.tokens);
+  }
+  __device__ void next_item(const ChunkArgs& a) {   // which exists
+    unit = 0;
+    if (++qt >= items) {
+      qt = 0;
+      if (++h == a.n_kv) {
+        h = 0;
+        do {
+          ++s;
+          load_stream(a);
+        } while (n == 0);
+      }
+    }
+    x = item_of(a, n, len, qt);
+  }
+};
+
+// Walks the segments (runs of units of one item) of the CTA's run [u0, u1).
+template <typename F>
+__device__ __forceinline__ void for_segments(const ChunkArgs& a, ChunkPlace p, int64_t u0, int64_t u1, F&& f) {
+  int seg = 0;
+  for (int64_t u = u0; u < u1; ++seg) {
+    const int t0 = p.unit, t1 = (int)min((int64_t)p.x.units, p.unit + (u1 - u));
+    if (!f(p, seg, t0, t1, u - t0)) return;
+    u += t1 - t0;
+    if (u < u1) p.next_item(a);
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __grid_constant__ ChunkArgs a) {
+  using Shape = ChunkShape<D>;
+  constexpr int STAGES = Shape::STAGES, TILE = Shape::TILE, HALVES = D / 64, HALF_TILE = TILE / HALVES;
+  extern __shared__ char smem_raw[];
+  __shared__ alignas(8) uint64_t bars[10 + 3 * STAGES];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int stop_sh, ticket_sh;
+  __shared__ int poison[16];
+  __shared__ int64_t warp_total[CHUNK_THREADS / 32];
+  __shared__ ChunkPlace start_sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  volatile int* stop = &stop_sh;
+  int* status = a.c.status;
+  const uint32_t smem0 = (smem_address(smem_raw) + 1023) & ~1023u;
+  const uint32_t q_smem = smem0, ring = smem0 + 2 * TILE;
+  const uint32_t bar0 = smem_address(bars);
+  const uint32_t q_full = bar0, q_free = bar0 + 8;
+  auto full = [&](int i) { return bar0 + 8 * (2 + i); };
+  auto clean = [&](int i) { return bar0 + 8 * (2 + STAGES + i); };
+  auto empty = [&](int i) { return bar0 + 8 * (2 + 2 * STAGES + i); };
+  auto s_full = [&](int i) { return bar0 + 8 * (2 + 3 * STAGES + i); };
+  auto p_full = [&](int i) { return bar0 + 8 * (4 + 3 * STAGES + i); };
+  const uint32_t joined = bar0 + 8 * (6 + 3 * STAGES), counted = bar0 + 8 * (7 + 3 * STAGES);
+  auto o_seen = [&](int i) { return bar0 + 8 * (8 + 3 * STAGES + i); };
+
+  if (warp == 9) tmem_alloc(smem_address(&tmem_base_sh), 512);
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(clean(i), 2);
+      mbar_init(empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(p_full(i), 4);
+      mbar_init(o_seen(i), 4);
+    }
+    mbar_init(joined, 8);
+    mbar_init(counted, 1);
+    stop_sh = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid < 16) poison[tid] = -1;
+
+  // The line: units of one key head before every stream, in the ring's memory (which holds no tile yet).
+  int64_t* before = (int64_t*)(smem_raw + (ring - smem_address(smem_raw)));
+  const int S = a.b.streams, item_tokens = 2 * a.tokens;
+  {
+    // few items per stream: a thread each; many: a warp each
+    for (int s = tid; s < S; s += CHUNK_THREADS) {
+      const int n = a.b.count(s);
+      if (n > 4 * item_tokens) continue;
+      const int len = a.c.length(s, blockIdx.x == 0);
+      int64_t sum = 0;
+      for (int qt = 0; qt * item_tokens < n; ++qt) sum += item_of(a, n, len, qt).units;
+      before[s] = sum;
+    }
+    for (int s = warp; s < S; s += CHUNK_THREADS / 32) {
+      const int n = a.b.count(s);
+      if (n <= 4 * item_tokens) continue;
+      const int len = a.c.length(s, blockIdx.x == 0 && lane == 0);
+      int64_t all = 0;
+      for (int qt = lane; qt * item_tokens < n; qt += 32) all += item_of(a, n, len, qt).units;
+      for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(~0u, all, d);
+      if (lane == 0) before[s] = all;
+    }
+    __syncthreads();
+    // exclusive prefix sums, a run of streams per thread
+    const int per = (S + CHUNK_THREADS - 1) / CHUNK_THREADS;
+    int64_t sum = 0;
+    for (int i = 0; i < per; ++i)
+      if (tid * per + i < S) sum += before[tid * per + i];
+    int64_t run = sum;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, run, d);
+      if (lane >= d) run += y;
+    }
+    if (lane == 31) warp_total[warp] = run;
+    __syncthreads();
+    run -= sum;
+    for (int w = 0; w < warp; ++w) run += warp_total[w];
+    for (int i = 0; i < per; ++i) {
+      const int s = tid * per + i;
+      if (s < S) {
+        const int64_t own = before[s];
+        before[s] = run;
+        run += own;
+        if (s == S - 1) before[S] = run;
+      }
+    }
+    __syncthreads();
+  }
+  const int64_t total = before[S] * a.n_kv;
+  const int64_t quota = max((int64_t)CHUNK_MIN_UNITS, (total + gridDim.x - 1) / gridDim.x);
+  const int64_t u0 = min(total, (int64_t)blockIdx.x * quota), u1 = min(total, u0 + quota);
+  if (tid == 0 && u0 < u1) {
+    int lo = 0, hi = S - 1;   // last stream that begins at or before u0 (so it has units)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (before[mid] * a.n_kv <= u0) lo = mid;
+      else hi = mid - 1;
+    }
+    ChunkPlace p;
+    p.s = lo;
+    p.load_stream(a);
+    int64_t left = u0 - before[lo] * a.n_kv;
+    const int64_t per_head = before[lo + 1] - before[lo];
+    p.h = (int)(left / per_head);
+    left -= p.h * per_head;
+    p.qt = 0;
+    p.x = item_of(a, p.n, p.len, 0);
+    while (left >= p.x.units) {
+      left -= p.x.units;
+      p.x = item_of(a, p.n, p.len, ++p.qt);
+    }
+    p.unit = (int)left;
+    start_sh = p;
+  }
+  fence_async_smem();   // the prefix sums were written by ordinary stores, tiles come through TMA
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  const ChunkPlace start = start_sh;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 8) {
+      // ---- copies ----
+      int stage = 0, q_uses = 0;
+      uint32_t phase = 0;
+      const int in_page = (1 << a.c.page_shift) - 1;
+      const int boxes = TILE_KEYS / a.box_keys;                  // per tile and 64 columns
+      const uint32_t box_bytes = a.box_keys * 128;
+      for_segments(a, start, u0, u1, [&](const ChunkPlace& p, int, int t0, int t1, int64_t) {
+        if (q_uses > 0 && !mbar_wait(q_free, (q_uses - 1) & 1, stop, status)) return false;
+        ++q_uses;
+        const int tiles = p.x.count > a.tokens ? 2 : 1;
+        if (lane == 0) {
+          const int row = a.b.begin(p.s) + p.x.i0;
+          mbar_expect(q_full, tiles * HALVES * a.tokens * a.group * 128);
+          for (int i = 0; i < tiles; ++i)
+            for (int c = 0; c < HALVES; ++c)
+              tma_load_3d(q_smem + i * TILE + c * HALF_TILE, &a.q_map, 64 * c, p.h * a.group, row + i * a.tokens, q_full);
+        }
+        for (int t = t0; t < t1; ++t) {
+          const int key0 = (p.x.begin + t) * TILE_KEYS;
+          // lane -> (box, 64-column half); boxes without a seen slot are left out
+          const int box = lane / HALVES, half = lane % HALVES, key = key0 + box * a.box_keys;
+          const bool want = box < boxes && key < p.x.hi && key + a.box_keys > p.x.lo;
+          int page = -1;
+          if (want) {
+            page = a.c.page(p.s, key >> a.c.page_shift);
+            if (page < 0) a.c.flag();
+          }
+          const uint32_t live = __ballot_sync(~0u, page >= 0);
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!mbar_wait(empty(stage), phase ^ 1, stop, status)) return false;
+            if (lane == 0) mbar_expect(full(stage), __popc(live) * box_bytes);
+            __syncwarp();
+            if (page >= 0)
+              tma_load_4d(ring + stage * TILE + half * HALF_TILE + box * box_bytes, kv ? &a.v_map : &a.k_map, 64 * half,
+                          key & in_page, p.h, page, full(stage));
+            if (++stage == STAGES) stage = 0, phase ^= 1;
+          }
+        }
+        return true;
+      });
+    } else if (warp == 9) {
+      // ---- products ----
+      int stage = 0;          // of the next tile in the ring
+      uint32_t phase = 0, q_phase = 0;
+      uint32_t p_phase[2] = {0, 0}, o_phase[2] = {1, 1};
+      constexpr uint32_t KIND_S = mma_kind<T>(TILE_ROWS, TILE_KEYS, false), KIND_O = mma_kind<T>(TILE_ROWS, D, true);
+      auto next = [&] {
+        if (++stage == STAGES) stage = 0, phase ^= 1;
+      };
+      auto scores = [&](int i, uint32_t k) {
+        if (lane == 0) {
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const uint32_t off = (j & 3) * 32 + (j >> 2) * HALF_TILE;
+            mma_ss(tmem + 128 * i, desc_k_major(q_smem + i * TILE + off), desc_k_major(k + off), KIND_S, j > 0);
+          }
+          mma_commit(s_full(i));
+        }
+      };
+      auto values = [&](int i, uint32_t v, bool add) {
+        if (lane == 0) {
+#pragma unroll
+          for (int j = 0; j < TILE_KEYS / 16; ++j)
+            mma_ts(tmem + Shape::O_COLUMN + 128 * i, tmem + 128 * i + 8 * j, desc_n_major(v + j * 2048, HALF_TILE), KIND_O,
+                   add || j > 0);
+        }
+      };
+      for_segments(a, start, u0, u1, [&](const ChunkPlace& p, int, int t0, int t1, int64_t) {
+        const int tiles = p.x.count > a.tokens ? 2 : 1;
+        if (!mbar_wait(q_full, q_phase, stop, status)) return false;
+        q_phase ^= 1;
+        int k_stage = stage;
+        if (!mbar_wait(full(k_stage), phase, stop, status)) return false;
+        next();
+        tmem_fence_after();
+        for (int i = 0; i < tiles; ++i) {
+          // the softmax has to have seen the end of the tile's last item: two unseen phases would look like none
+          if (!mbar_wait(o_seen(i), o_phase[i], stop, status)) return false;
+          o_phase[i] ^= 1;
+          scores(i, ring + k_stage * TILE);
+        }
+        if (lane == 0) mma_commit(empty(k_stage));
+        for (int t = t0; t < t1; ++t) {
+          const int v_stage = stage;
+          if (!mbar_wait(clean(v_stage), phase, stop, status) || !mbar_wait(full(v_stage), phase, stop, status)) return false;
+          next();
+          const bool more = t + 1 < t1;
+          if (more) {
+            k_stage = stage;
+            if (!mbar_wait(full(k_stage), phase, stop, status)) return false;
+            next();
+          }
+          for (int i = 0; i < tiles; ++i) {
+            if (!mbar_wait(p_full(i), p_phase[i], stop, status)) return false;
+            p_phase[i] ^= 1;
+            tmem_fence_after();
+            values(i, ring + v_stage * TILE, t > t0);
+            if (more) scores(i, ring + k_stage * TILE);           // after the weights that it overwrites were read
+            else if (lane == 0) mma_commit(s_full(i));            // the accumulator is complete
+          }
+          if (lane == 0) {
+            mma_commit(empty(v_stage));
+            if (more) mma_commit(empty(k_stage));
+            else mma_commit(q_free);
+          }
+          __syncwarp();
+        }
+        return true;
+      });
+    } else {
+      // ---- clean values ----
+      int stage = 0;
+      uint32_t phase = 0;
+      auto next = [&] {
+        if (++stage == STAGES) stage = 0, phase ^= 1;
+      };
+      const int id = tid - 320;
+      for_segments(a, start, u0, u1, [&](const ChunkPlace& p, int seg, int t0, int t1, int64_t) {
+        for (int t = t0; t < t1; ++t) {
+          if (lane == 0) mbar_arrive(clean(stage));   // keys need none; their stage's phase moves on all the same
+          next();
+          if (!mbar_wait(full(stage), phase, stop, status)) return false;
+          const int key0 = (p.x.begin + t) * TILE_KEYS;
+          const int dead_lo = p.x.lo - key0, dead_hi = p.x.hi - key0;
+          const bool some_dead = dead_lo > 0 || dead_hi < TILE_KEYS;
+          // seen by some rows only
+          const bool mixed = (key0 < p.x.last.x && key0 + TILE_KEYS > p.x.first.x) ||
+                             (key0 < p.x.last.y && key0 + TILE_KEYS > p.x.first.y);
+          if (some_dead || mixed) {
+            bool bad = false;
+            for (int c = id; c < TILE_KEYS * D / 8; c += 64) {     // 16-byte pieces
+              const int r = (c >> 3) & (TILE_KEYS - 1), key = key0 + r;
+              const uint32_t at = ring + stage * TILE + c * 16;
+              if (r < dead_lo || r >= dead_hi) {
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+              } else if ((key < p.x.last.x) || (key >= p.x.first.y)) {
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+                uint32_t keep = 0xffffffffu;
+                constexpr uint32_t E = Half2<T>::EXPONENT;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint32_t k = 0xffffffffu;
+                  if ((w[e] & E & 0xffffu) == (E & 0xffffu)) k &= 0xffff0000u;
+                  if ((w[e] & E & 0xffff0000u) == (E & 0xffff0000u)) k &= 0xffffu;
+                  w[e] &= k;
+                  keep &= k;
+                }
+                if (keep != 0xffffffffu) {
+                  bad = true;
+                  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+                }
+              }
+            }
+            if (bad) *(volatile int*)&poison[seg & 15] = seg;
+            fence_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(clean(stage));
+          next();
+        }
+        return true;
+      });
+    }
+  } else {
+    // ---- softmax ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int tile = warp >> 2, row = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 lanes
+    const uint32_t s_tmem = lanes + 128 * tile, o_tmem = lanes + Shape::O_COLUMN + 128 * tile;
+    const float sc = a.scale * LOG2E;
+    uint32_t s_phase = 0, join_phase = 0;
+    for_segments(a, start, u0, u1, [&](const ChunkPlace& p, int seg, int t0, int t1, int64_t item_begin) {
+      const bool whole = t0 == 0 && t1 == p.x.units;
+      const int tok = row / a.group, count = p.x.count - tile * a.tokens;   // tokens of this tile
+      const bool valid = tok < min(count, a.tokens);
+      const int i = p.x.i0 + tile * a.tokens + tok;                         // token in the push
+      const int2 mine = valid ? seen(p.len, p.n, i, a.causal, a.window) : make_int2(0, 0);
+      float m = -INFINITY, l = 0.f;
+      if (count > 0) {
+        const int i_first = p.x.i0 + tile * a.tokens, i_last = i_first + min(count, a.tokens) - 1;
+        const int all_lo = seen(p.len, p.n, i_last, a.causal, a.window).x;
+        const int all_hi = seen(p.len, p.n, i_first, a.causal, a.window).y;
+        for (int t = t0; t < t1; ++t) {
+          const int key0 = (p.x.begin + t) * TILE_KEYS;
+          if (!mbar_wait(s_full(tile), s_phase, stop, status)) return false;
+          s_phase ^= 1;
+          tmem_fence_after();
+          uint32_t x[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_load32(x + 32 * c, s_tmem + 32 * c);
+          tmem_wait_load();
+          if (key0 < all_lo || key0 + TILE_KEYS > all_hi) {
+            const int lo = mine.x - key0, hi = mine.y - key0;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c < lo || c >= hi) x[c] = 0xff800000u;
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 128; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              top[e] = fmaxf(top[e], fmaxf(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])));
+          const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+          const bool grow = high > m + RESCALE_AT || (m == -INFINITY && high > m);
+          if (__any_sync(~0u, grow)) {
+            const float f = grow ? exp2_approx(m - high) : 1.f;
+            if (grow) {
+              m = high;
+              l *= f;
+            }
+            if (t > t0) {   // the product before this one is complete: its scores came after it
+#pragma unroll
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_load16(o, o_tmem + c);
+                tmem_wait_load();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_store16(o_tmem + c, o);
+              }
+            }
+          }
+          const float use = m == -INFINITY ? 0.f : m;
+          const uint64_t sc2 = pack2(sc, sc), use2 = pack2(-use, -use);
+          uint64_t sum = pack2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = unpack2(fma2(pack2(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), sc2, use2));
+              const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
+              sum = add2(sum, pack2(p0, p1));                 // before the weights are rounded to the rows' type
+              w[e] = Half2<T>::from_float(p0, p1);
+            }
+            tmem_store16(s_tmem + c / 2, w);
+          }
+          tmem_wait_store();
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(tile));
+          const float2 both = unpack2(sum);
+          l += both.x + both.y;
+        }
+        if (!mbar_wait(s_full(tile), s_phase, stop, status)) return false;   // the accumulator is complete
+        s_phase ^= 1;
+        if (lane == 0) mbar_arrive(o_seen(tile));
+        tmem_fence_after();
+      }
+      // values that were taken out, for the rows that see them
+      const bool fix = *(volatile int*)&poison[seg & 15] == seg;
+      const int k_lo = (p.x.begin + t0) * TILE_KEYS, k_hi = (p.x.begin + t1) * TILE_KEYS;
+      auto add_taken_out = [&](float* o, int c0) {
+        const int2 parts[2] = {make_int2(max(mine.x, k_lo), min(min(mine.y, k_hi), p.x.last.x)),
+                               make_int2(max(max(mine.x, k_lo), max(p.x.first.y, p.x.last.x)), min(mine.y, k_hi))};
+        for (int z = 0; z < 2; ++z)
+          for (int key = parts[z].x; key < parts[z].y; ++key) {
+            const int page = a.c.page(p.s, key >> a.c.page_shift);
+            if (page < 0) continue;
+            const T* v = (const T*)a.c.v + page * a.c.v_page + p.h * a.c.v_head + (key & ((1 << a.c.page_shift) - 1)) * a.c.v_slot;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float y = (float)v[c0 + c];
+              if (!(fabsf(y) < INFINITY)) o[c] += y;
+            }
+          }
+      };
+      const int64_t t_row = a.b.begin(p.s) + i;
+      const int hq = p.h * a.group + row - tok * a.group;
+      if (whole) {
+        if (count > 0) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          T* out = (T*)a.out.data + t_row * a.out.row + (int64_t)hq * a.out.head;
+#pragma unroll
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_load16(o, o_tmem + c);
+            tmem_wait_load();
+            float y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+            if (fix) add_taken_out(y, c);
+            if (valid) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = Half2<T>::from_float(y[2 * e], y[2 * e + 1]);
+              *(uint4*)(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+              *(uint4*)(out + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+          if (valid && a.lse) a.lse[t_row * a.n_q + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+        }
+        return true;
+      }
+      // slot 0: an item that began before this run; slot 1: one that began in it
+      const int item_row = tile * TILE_ROWS + row;
+      {
+        float* part = a.parts + (int64_t)(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * Shape::PART;
+        if (valid) {
+          __stcg(part + item_row, m);
+          __stcg(part + ITEM_ROWS + item_row, l);
+        }
+        if (count > 0) {
+#pragma unroll
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_load16(o, o_tmem + c);
+            tmem_wait_load();
+            float y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(o[e]);
+            if (fix) add_taken_out(y, c);
+            if (valid)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                __stcg((float4*)(part + 2 * ITEM_ROWS) + (c / 4 + e) * ITEM_ROWS + item_row,
+                       make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]));
+          }
+        }
+      }
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(joined);
+      const int first = (int)(item_begin / quota), last = (int)((item_begin + p.x.units - 1) / quota);
+      if (tid == 0 && mbar_wait_thread(joined, join_phase, stop, status)) {
+        const int done = atomicAdd(a.tickets + first, 1);
+        if (done == last - first) a.tickets[first] = 0;   // ready for the next call
+        ticket_sh = done;
+        mbar_arrive(counted);
+      }
+      __syncwarp();
+      if (!mbar_wait(counted, join_phase, stop, status)) return false;
+      join_phase ^= 1;
+      if (*(volatile int*)&ticket_sh == last - first) {
+        __threadfence();
+        auto slot = [&](int w) { return a.parts + (int64_t)(2 * w + (w == first ? 1 : 0)) * Shape::PART; };
+        const int rows = p.x.count > a.tokens ? ITEM_ROWS : TILE_ROWS;
+        for (int u = tid; u < rows * (D / 4); u += 256) {   // a thread keeps to one row: 256 is a multiple of the rows
+          const int r = u % rows, d4 = u / rows;
+          const int tk = (r & 127) / a.group, j = (r >> 7) * a.tokens + tk;
+          if (tk >= a.tokens || j >= p.x.count) continue;
+          float mm = -INFINITY;
+          for (int w = first; w <= last; ++w) mm = fmaxf(mm, __ldcg(slot(w) + r));
+          const float base = mm == -INFINITY ? 0.f : mm;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float sum = 0.f;
+#pragma unroll 4
+          for (int w = first; w <= last; ++w) {
+            const float* sl = slot(w);
+            const float f = exp2_approx(__ldcg(sl + r) - base);
+            const float4 y = __ldcg((const float4*)(sl + 2 * ITEM_ROWS) + d4 * ITEM_ROWS + r);
+            sum += f * __ldcg(sl + ITEM_ROWS + r);
+            acc.x += f * y.x;
+            acc.y += f * y.y;
+            acc.z += f * y.z;
+            acc.w += f * y.w;
+          }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const int64_t tr = a.b.begin(p.s) + p.x.i0 + j;
+          const int head = p.h * a.group + (r & 127) - tk * a.group;
+          uint2 w = make_uint2(Half2<T>::from_float(acc.x * inv, acc.y * inv), Half2<T>::from_float(acc.z * inv, acc.w * inv));
+          if (sum == 0.f) w = make_uint2(0u, 0u);
+          *(uint2*)((T*)a.out.data + tr * a.out.row + (int64_t)head * a.out.head + 4 * d4) = w;
+          if (a.lse && d4 == 0) a.lse[tr * a.n_q + head] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * LN2;
+        }
+      }
+      return true;
+    });
+  }
+  // a wait that ran out leaves copies and products behind: give them time before their memory goes
+  if (*stop)
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_free(tmem, 512);
+}
+
+}  // namespace cache
+}  // namespace logmel
