@@ -231,11 +231,12 @@ size_t parts_bytes(const logmel_cache_plan* p) {
 
 template <typename T, int D>
 cudaError_t allow_shared_memory() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(attend_rows_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsShape<D>::SMEM);
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(attend_chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 ChunkShape<D>::SMEM);
+  constexpr cudaFuncAttribute LIMIT = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<T, D>, LIMIT, RowsShape<D>::SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(attend_chunk_kernel<T, D>, LIMIT, ChunkShape<D>::SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(weigh_kernel<T, D, 16>, LIMIT, WeighShape<D, 16>::SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(weigh_kernel<T, D, 128>, LIMIT, WeighShape<D, 128>::SMEM);
+  return e;
 }
 
 CUtensorMapDataType element_type(const logmel_cache_plan* p) {
@@ -291,6 +292,23 @@ logmel_status launch_attend(const logmel_cache_plan* p, const AttendArgs& a, int
     attend_chunk_kernel<T, D><<<p->sms, CHUNK_THREADS, ChunkShape<D>::SMEM, str>>>(x);
   }
   return launched(__LINE__);
+}
+
+template <typename T, int D, int N>
+logmel_status launch_weigh_columns(const logmel_cache_plan* p, WeighArgs& a, cudaStream_t str) {
+  a.tokens = N / p->group;
+  a.box_keys = std::min(p->cfg.page_size, TILE_KEYS);
+  const CacheView& c = a.c;
+  if (!encode_rows(p, &a.q_map, a.q, a.b.rows, a.n_q, a.tokens) ||
+      !encode_pages(p, &a.k_map, c.k, c.n_pages, c.k_page, c.k_head, c.k_slot, a.box_keys))
+    return no_map(__LINE__);
+  weigh_kernel<T, D, N><<<p->sms, CHUNK_THREADS, WeighShape<D, N>::SMEM, str>>>(a);
+  return launched(__LINE__);
+}
+
+template <typename T, int D>
+logmel_status launch_weigh(const logmel_cache_plan* p, WeighArgs& a, int64_t most, cudaStream_t str) {
+  return most * p->group <= 16 ? launch_weigh_columns<T, D, 16>(p, a, str) : launch_weigh_columns<T, D, 128>(p, a, str);
 }
 
 }  // namespace
@@ -484,15 +502,13 @@ logmel_status logmel_cache_weigh(logmel_cache_plan* p, const logmel_cache_view* 
     a.q = device_rows(*q, r0);
     a.lse = lse + r0 * c.n_q_heads;
     const cudaStream_t str = (cudaStream_t)stream;
-    const dim3 grid(64, c.n_kv_heads, a.b.streams);
     if (c.dtype == LOGMEL_BF16) {
-      if (c.head_dim == 128) weigh_simple_kernel<__nv_bfloat16, 128><<<grid, 128, 0, str>>>(a);
-      else weigh_simple_kernel<__nv_bfloat16, 64><<<grid, 128, 0, str>>>(a);
+      st = c.head_dim == 128 ? launch_weigh<__nv_bfloat16, 128>(p, a, it.most, str)
+                             : launch_weigh<__nv_bfloat16, 64>(p, a, it.most, str);
     } else {
-      if (c.head_dim == 128) weigh_simple_kernel<__half, 128><<<grid, 128, 0, str>>>(a);
-      else weigh_simple_kernel<__half, 64><<<grid, 128, 0, str>>>(a);
+      st = c.head_dim == 128 ? launch_weigh<__half, 128>(p, a, it.most, str) : launch_weigh<__half, 64>(p, a, it.most, str);
     }
-    if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
+    if (st != LOGMEL_OK) return st;
   }
   return LOGMEL_OK;
 }

@@ -31,6 +31,7 @@ constexpr int TILE_KEYS = 128;
 constexpr int CHUNK_THREADS = 384;
 constexpr int CHUNK_MIN_UNITS = 2;
 constexpr float RESCALE_AT = 8.f;   // in powers of two
+constexpr uint32_t FIT_PAIRS = 0x4a94;   // of every 16 pairs of weights, those computed on the FMA pipe
 
 template <int D>
 struct ChunkShape {
@@ -430,7 +431,8 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_load32(x + 32 * c, s_tmem + 32 * c);
           tmem_wait_load();
-          if (key0 < all_lo || key0 + TILE_KEYS > all_hi) {
+          bool plain = key0 >= all_lo && key0 + TILE_KEYS <= all_hi;   // every row sees every key
+          if (!plain) {
             const int lo = mine.x - key0, hi = mine.y - key0;
 #pragma unroll
             for (int c = 0; c < 128; ++c)
@@ -441,15 +443,17 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
           for (int c = 0; c < 128; c += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              top[e] = fmaxf(top[e], fmaxf(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])));
-          const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
-          const bool grow = high > m + RESCALE_AT || (m == -INFINITY && high > m);
+              top[e] = max3_nan(top[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
+          // rows past the item's hold whatever the tile holds there: they must not choose the warp's path
+          const float high = valid ? max3_nan(max3_nan(top[0], top[1], top[2]), top[3], top[3]) * sc : -INFINITY;
+          const bool grow = !(high <= m + RESCALE_AT);   // also where high is NaN
           if (__any_sync(~0u, grow)) {
             const float f = grow ? exp2_approx(m - high) : 1.f;
             if (grow) {
               m = high;
               l *= f;
             }
+            plain = plain && !__any_sync(~0u, !(high < INFINITY));
             if (t > t0) {   // the product before this one is complete: its scores came after it
 #pragma unroll
               for (int c = 0; c < D; c += 16) {
@@ -465,17 +469,39 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
           const float use = m == -INFINITY ? 0.f : m;
           const uint64_t sc2 = pack2(sc, sc), use2 = pack2(-use, -use);
           uint64_t sum = pack2(0.f, 0.f);
+          // sums before the weights are rounded to the rows' type
+          if (plain) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t w[16];
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 y = unpack2(fma2(pack2(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), sc2, use2));
-              const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
-              sum = add2(sum, pack2(p0, p1));                 // before the weights are rounded to the rows' type
-              w[e] = Half2<T>::from_float(p0, p1);
+              for (int e = 0; e < 16; ++e) {
+                const uint64_t y = fma2(pack2(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), sc2, use2);
+                float2 pw;
+                if (FIT_PAIRS >> e & 1) {
+                  pw = unpack2(exp2_fit(y));
+                } else {
+                  const float2 z = unpack2(y);
+                  pw = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+                }
+                sum = add2(sum, pack2(pw.x, pw.y));
+                w[e] = Half2<T>::from_float(pw.x, pw.y);
+              }
+              tmem_store16(s_tmem + c / 2, w);
             }
-            tmem_store16(s_tmem + c / 2, w);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float p0 = exp2_approx(fmaf(__uint_as_float(x[c + 2 * e]), sc, -use));
+                const float p1 = exp2_approx(fmaf(__uint_as_float(x[c + 2 * e + 1]), sc, -use));
+                sum = add2(sum, pack2(p0, p1));
+                w[e] = Half2<T>::from_float(p0, p1);
+              }
+              tmem_store16(s_tmem + c / 2, w);
+            }
           }
           tmem_wait_store();
           tmem_fence_before();

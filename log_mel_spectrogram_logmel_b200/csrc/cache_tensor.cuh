@@ -18,6 +18,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// The larger of three, NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // --- mbarriers ---------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint32_t bar, int count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -177,6 +184,30 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// 2^x of two values on the FMA pipe, for finite x <= 100 or so; below -126
+// the result stays at 2^-126 (callers send masked and other infinite or NaN
+// values through ex2).  x = n + f with n the nearest integer (adding
+// 1.5 x 2^23 leaves n in the low bits), f in [-1/2, 1/2]; 2^f by the polynomial of
+// degree 4 of least relative error there (fitted by reweighted least squares,
+// 2.7e-6 in fp32), and n goes into the exponent by an integer addition.
+// The special-function unit gives 16 exponentials a clock and SM, a quarter
+// of what the softmax of one tile needs while the tensor cores make the next,
+// so a share of them goes this way.
+__device__ __forceinline__ uint64_t exp2_fit(uint64_t x) {
+  const float2 y = unpack2(x);
+  const uint64_t z = pack2(fmaxf(y.x, -126.f), fmaxf(y.y, -126.f));
+  const uint64_t shift = pack2(12582912.f, 12582912.f), unshift = pack2(-12582912.f, -12582912.f);
+  const uint64_t t = add2(z, shift);
+  const uint64_t f = fma2(add2(t, unshift), pack2(-1.f, -1.f), z);
+  uint64_t p = fma2(f, pack2(0x1.3997d6p-7f, 0x1.3997d6p-7f), pack2(0x1.ca1440p-5f, 0x1.ca1440p-5f));
+  p = fma2(p, f, pack2(0x1.ec06dap-3f, 0x1.ec06dap-3f));
+  p = fma2(p, f, pack2(0x1.62e0dcp-1f, 0x1.62e0dcp-1f));
+  p = fma2(p, f, pack2(0x1.ffffe8p-1f, 0x1.ffffe8p-1f));
+  const float2 n = unpack2(t), v = unpack2(p);
+  return pack2(__uint_as_float(__float_as_uint(v.x) + (__float_as_uint(n.x) << 23)),
+               __uint_as_float(__float_as_uint(v.y) + (__float_as_uint(n.y) << 23)));
 }
 
 }  // namespace cache
