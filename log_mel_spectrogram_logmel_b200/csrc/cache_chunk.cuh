@@ -30,6 +30,8 @@ constexpr int ITEM_ROWS = 2 * TILE_ROWS;
 constexpr int TILE_KEYS = 128;
 constexpr int CHUNK_THREADS = 384;
 constexpr int CHUNK_MIN_UNITS = 2;
+constexpr int MAX_CTAS = 160;
+constexpr int WAVES_MAX = 5;        // beyond, the few split items of the one line do not matter
 constexpr float RESCALE_AT = 8.f;   // in powers of two
 constexpr uint32_t FIT_PAIRS = 0x4a94;   // of every 16 pairs of weights, those computed on the FMA pipe
 
@@ -95,10 +97,28 @@ struct ChunkPlace {
   }
 };
 
-// Walks the segments (runs of units of one item) of the CTA's run [u0, u1).
+// Item `i` of the launch where every stream has as many new tokens.
+__device__ __forceinline__ ChunkPlace place_of_item(const ChunkArgs& a, int i) {
+  const int items = (a.b.uniform + 2 * a.tokens - 1) / (2 * a.tokens);
+  ChunkPlace p;
+  p.s = i / (items * a.n_kv);
+  p.load_stream(a);
+  const int r = i - p.s * items * a.n_kv;
+  p.h = r / items;
+  p.qt = r - p.h * items;
+  p.unit = 0;
+  p.x = item_of(a, p.n, p.len, p.qt);
+  return p;
+}
+
+// Walks the CTA's segments (runs of units of one item): its whole items, then its run [u0, u1) from `p` on.
 template <typename F>
-__device__ __forceinline__ void for_segments(const ChunkArgs& a, ChunkPlace p, int64_t u0, int64_t u1, F&& f) {
+__device__ __forceinline__ void for_segments(const ChunkArgs& a, int waves, ChunkPlace p, int64_t u0, int64_t u1, F&& f) {
   int seg = 0;
+  for (; seg < waves; ++seg) {
+    const ChunkPlace w = place_of_item(a, seg * gridDim.x + blockIdx.x);
+    if (!f(w, seg, 0, w.x.units, (int64_t)0)) return;
+  }
   for (int64_t u = u0; u < u1; ++seg) {
     const int t0 = p.unit, t1 = (int)min((int64_t)p.x.units, p.unit + (u1 - u));
     if (!f(p, seg, t0, t1, u - t0)) return;
@@ -118,6 +138,8 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
   __shared__ int poison[16];
   __shared__ int64_t warp_total[CHUNK_THREADS / 32];
   __shared__ ChunkPlace start_sh;
+  __shared__ int64_t run_end_sh;
+  __shared__ int bound[MAX_CTAS + 1];   // where the runs begin, if whole items go first
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* stop = &stop_sh;
   int* status = a.c.status;
@@ -204,26 +226,95 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
   }
   const int64_t total = before[S] * a.n_kv;
   const int64_t quota = max((int64_t)CHUNK_MIN_UNITS, (total + gridDim.x - 1) / gridDim.x);
-  const int64_t u0 = min(total, (int64_t)blockIdx.x * quota), u1 = min(total, u0 + quota);
-  if (tid == 0 && u0 < u1) {
-    int lo = 0, hi = S - 1;   // last stream that begins at or before u0 (so it has units)
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (before[mid] * a.n_kv <= u0) lo = mid;
-      else hi = mid - 1;
+
+  // Where all streams push the same and there are some whole items for every
+  // CTA, these go first, one per CTA at a time in the order of the line: CTAs of the
+  // same keys then read them at the same time, from L2.  What is left is cut so
+  // that every CTA ends up with its quota.  (Cut as one line, 4,096 rows over 65,536 slots
+  // read 6.3 GB from memory for 0.27 GB of keys and values.)
+  const int G = gridDim.x;
+  int waves = 0, n_items = 0;
+  if (a.b.uniform > 0) {
+    const int64_t all = (int64_t)S * a.n_kv * ((a.b.uniform + item_tokens - 1) / item_tokens);
+    if (G <= MAX_CTAS && all >= G && all <= WAVES_MAX * G) {
+      n_items = (int)all;
+      waves = n_items / G;
     }
+  }
+  if (waves > 0) {
+    bool over = false;
+    if (tid < G) {
+      int64_t own = 0;
+      for (int w = 0; w < waves; ++w) own += place_of_item(a, w * G + tid).x.units;
+      over = own > quota;
+      bound[tid + 1] = (int)(quota - own);   // room left; below 2^31: a length is
+    }
+    if (__syncthreads_or(over)) {
+      waves = 0;
+    } else {
+      if (warp == 0) {   // prefix sums
+        int carry = 0;
+        for (int i = 0; i < G; i += 32) {
+          int v = i + lane < G ? bound[i + lane + 1] : 0;
+          for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(~0u, v, d);
+            if (lane >= d) v += y;
+          }
+          if (i + lane < G) bound[i + lane + 1] = carry + v;
+          carry += __shfl_sync(~0u, v, 31);
+        }
+        if (lane == 0) bound[0] = 0;
+      }
+      __syncthreads();
+    }
+  }
+  // this CTA's run of the line (of what is left of it)
+  int64_t u0 = (int64_t)blockIdx.x * quota, u1 = u0 + quota, line = total;
+  if (waves > 0) {
+    u0 = bound[blockIdx.x];
+    u1 = bound[blockIdx.x + 1];
+    line = 0x7fffffffffffffff;   // its end is where the items end
+  }
+  u0 = min(u0, line);
+  u1 = min(u1, line);
+  if (tid == 0 && u0 < u1) {
     ChunkPlace p;
-    p.s = lo;
-    p.load_stream(a);
-    int64_t left = u0 - before[lo] * a.n_kv;
-    const int64_t per_head = before[lo + 1] - before[lo];
-    p.h = (int)(left / per_head);
-    left -= p.h * per_head;
-    p.qt = 0;
-    p.x = item_of(a, p.n, p.len, 0);
-    while (left >= p.x.units) {
-      left -= p.x.units;
-      p.x = item_of(a, p.n, p.len, ++p.qt);
+    int64_t left = u0;
+    if (waves > 0) {
+      int i = waves * G;
+      for (; i < n_items; ++i) {
+        p = place_of_item(a, i);
+        if (left < p.x.units) break;
+        left -= p.x.units;
+      }
+      // the last runs may reach past the last item
+      int64_t end = 0;
+      if (i < n_items) {
+        end = u0 - left;
+        for (int j = i; j < n_items && end < u1; ++j) end += place_of_item(a, j).x.units;
+      }
+      run_end_sh = min(u1, max(u0, end));
+      if (i == n_items) run_end_sh = u0;
+    } else {
+      int lo = 0, hi = S - 1;   // last stream that begins at or before u0 (so it has units)
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] * a.n_kv <= u0) lo = mid;
+        else hi = mid - 1;
+      }
+      p.s = lo;
+      p.load_stream(a);
+      left -= before[lo] * a.n_kv;
+      const int64_t per_head = before[lo + 1] - before[lo];
+      p.h = (int)(left / per_head);
+      left -= p.h * per_head;
+      p.qt = 0;
+      p.x = item_of(a, p.n, p.len, 0);
+      while (left >= p.x.units) {
+        left -= p.x.units;
+        p.x = item_of(a, p.n, p.len, ++p.qt);
+      }
+      run_end_sh = u1;
     }
     p.unit = (int)left;
     start_sh = p;
@@ -234,6 +325,17 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
   tmem_fence_after();
   const uint32_t tmem = tmem_base_sh;
   const ChunkPlace start = start_sh;
+  if (u0 < u1) u1 = run_end_sh;
+  auto owner = [&](int64_t u) {   // the CTA whose run holds unit u
+    if (waves == 0) return (int)(u / quota);
+    int lo = 0, hi = G - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (bound[mid] <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -244,7 +346,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
       const int in_page = (1 << a.c.page_shift) - 1;
       const int boxes = TILE_KEYS / a.box_keys;                  // per tile and 64 columns
       const uint32_t box_bytes = a.box_keys * 128;
-      for_segments(a, start, u0, u1, [&](const ChunkPlace& p, int, int t0, int t1, int64_t) {
+      for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int, int t0, int t1, int64_t) {
         if (q_uses > 0 && !mbar_wait(q_free, (q_uses - 1) & 1, stop, status)) return false;
         ++q_uses;
         const int tiles = p.x.count > a.tokens ? 2 : 1;
@@ -255,16 +357,19 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
             for (int c = 0; c < HALVES; ++c)
               tma_load_3d(q_smem + i * TILE + c * HALF_TILE, &a.q_map, 64 * c, p.h * a.group, row + i * a.tokens, q_full);
         }
+        // lane -> (box, 64-column half); boxes without a seen slot are left out
+        const int box = lane / HALVES, half = lane % HALVES;
+        auto page_of = [&](int t) {
+          const int key = (p.x.begin + t) * TILE_KEYS + box * a.box_keys;
+          if (t >= t1 || box >= boxes || key >= p.x.hi || key + a.box_keys <= p.x.lo) return -1;
+          const int page = a.c.page(p.s, key >> a.c.page_shift);
+          if (page < 0) a.c.flag();
+          return page;
+        };
+        int next_page = page_of(t0);
         for (int t = t0; t < t1; ++t) {
-          const int key0 = (p.x.begin + t) * TILE_KEYS;
-          // lane -> (box, 64-column half); boxes without a seen slot are left out
-          const int box = lane / HALVES, half = lane % HALVES, key = key0 + box * a.box_keys;
-          const bool want = box < boxes && key < p.x.hi && key + a.box_keys > p.x.lo;
-          int page = -1;
-          if (want) {
-            page = a.c.page(p.s, key >> a.c.page_shift);
-            if (page < 0) a.c.flag();
-          }
+          const int key = (p.x.begin + t) * TILE_KEYS + box * a.box_keys, page = next_page;
+          next_page = page_of(t + 1);   // a tile early: its latency hides behind the copies
           const uint32_t live = __ballot_sync(~0u, page >= 0);
           for (int kv = 0; kv < 2; ++kv) {
             if (!mbar_wait(empty(stage), phase ^ 1, stop, status)) return false;
@@ -288,7 +393,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
         if (++stage == STAGES) stage = 0, phase ^= 1;
       };
       auto scores = [&](int i, uint32_t k) {
-        if (lane == 0) {
+        if (elect_lane()) {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             const uint32_t off = (j & 3) * 32 + (j >> 2) * HALF_TILE;
@@ -298,14 +403,14 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
         }
       };
       auto values = [&](int i, uint32_t v, bool add) {
-        if (lane == 0) {
+        if (elect_lane()) {
 #pragma unroll
           for (int j = 0; j < TILE_KEYS / 16; ++j)
             mma_ts(tmem + Shape::O_COLUMN + 128 * i, tmem + 128 * i + 8 * j, desc_n_major(v + j * 2048, HALF_TILE), KIND_O,
                    add || j > 0);
         }
       };
-      for_segments(a, start, u0, u1, [&](const ChunkPlace& p, int, int t0, int t1, int64_t) {
+      for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int, int t0, int t1, int64_t) {
         const int tiles = p.x.count > a.tokens ? 2 : 1;
         if (!mbar_wait(q_full, q_phase, stop, status)) return false;
         q_phase ^= 1;
@@ -319,7 +424,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
           o_phase[i] ^= 1;
           scores(i, ring + k_stage * TILE);
         }
-        if (lane == 0) mma_commit(empty(k_stage));
+        if (elect_lane()) mma_commit(empty(k_stage));
         for (int t = t0; t < t1; ++t) {
           const int v_stage = stage;
           if (!mbar_wait(clean(v_stage), phase, stop, status) || !mbar_wait(full(v_stage), phase, stop, status)) return false;
@@ -336,9 +441,9 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
             tmem_fence_after();
             values(i, ring + v_stage * TILE, t > t0);
             if (more) scores(i, ring + k_stage * TILE);           // after the weights that it overwrites were read
-            else if (lane == 0) mma_commit(s_full(i));            // the accumulator is complete
+            else if (elect_lane()) mma_commit(s_full(i));            // the accumulator is complete
           }
-          if (lane == 0) {
+          if (elect_lane()) {
             mma_commit(empty(v_stage));
             if (more) mma_commit(empty(k_stage));
             else mma_commit(q_free);
@@ -355,9 +460,12 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
         if (++stage == STAGES) stage = 0, phase ^= 1;
       };
       const int id = tid - 320;
-      for_segments(a, start, u0, u1, [&](const ChunkPlace& p, int seg, int t0, int t1, int64_t) {
+      for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int seg, int t0, int t1, int64_t) {
         for (int t = t0; t < t1; ++t) {
-          if (lane == 0) mbar_arrive(clean(stage));   // keys need none; their stage's phase moves on all the same
+          // keys need no cleaning, but their stage's phase moves on all the same, no sooner than they are there:
+          // an arrival ahead of the products could pass the phase that they still have to see
+          if (!mbar_wait(full(stage), phase, stop, status)) return false;
+          if (lane == 0) mbar_arrive(clean(stage));
           next();
           if (!mbar_wait(full(stage), phase, stop, status)) return false;
           const int key0 = (p.x.begin + t) * TILE_KEYS;
@@ -411,7 +519,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
     const uint32_t s_tmem = lanes + 128 * tile, o_tmem = lanes + Shape::O_COLUMN + 128 * tile;
     const float sc = a.scale * LOG2E;
     uint32_t s_phase = 0, join_phase = 0;
-    for_segments(a, start, u0, u1, [&](const ChunkPlace& p, int seg, int t0, int t1, int64_t item_begin) {
+    for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int seg, int t0, int t1, int64_t item_begin) {
       const bool whole = t0 == 0 && t1 == p.x.units;
       const int tok = row / a.group, count = p.x.count - tile * a.tokens;   // tokens of this tile
       const bool valid = tok < min(count, a.tokens);
@@ -589,7 +697,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
       __threadfence();
       __syncwarp();
       if (lane == 0) mbar_arrive(joined);
-      const int first = (int)(item_begin / quota), last = (int)((item_begin + p.x.units - 1) / quota);
+      const int first = owner(item_begin), last = owner(item_begin + p.x.units - 1);
       if (tid == 0 && mbar_wait_thread(joined, join_phase, stop, status)) {
         const int done = atomicAdd(a.tickets + first, 1);
         if (done == last - first) a.tickets[first] = 0;   // ready for the next call

@@ -79,6 +79,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// One lane of a converged warp, always the same.  (The MMA's operands live in
+// uniform registers; behind a test of the lane number the compiler cannot
+// know that one thread is active, and issuing takes half as long again.)
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // --- tcgen05 -----------------------------------------------------------------
 // Shared-memory operands are tiles of 128-byte rows (64 16-bit elements) in
 // the 128-byte swizzle; 8 rows make an atom of 1024 bytes.

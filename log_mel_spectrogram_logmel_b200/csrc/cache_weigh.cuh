@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) weigh_kernel(const __grid_co
             if (!mbar_wait(s_free(t, buf), ((uses[t] >> 1) & 1) ^ 1, stop, status)) return false;
             ++uses[t];
             tmem_fence_after();
-            if (lane == 0) {
+            if (elect_lane()) {
               const uint32_t k = k_ring + k_stage[t] * Shape::K_TILE, q = q_ring + qs * Shape::Q_TILE;
 #pragma unroll
               for (int j = 0; j < D / 16; ++j)
@@ -288,10 +288,10 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) weigh_kernel(const __grid_co
             }
             __syncwarp();
           }
-          if (lane == 0) mma_commit(q_free(qs));
+          if (elect_lane()) mma_commit(q_free(qs));
           if (++qs == QS) qs = 0, q_phase ^= 1;
         }
-        if (lane == 0)
+        if (elect_lane())
           for (int t = 0; t < tiles; ++t) mma_commit(k_free(k_stage[t]));
         __syncwarp();
         return true;
