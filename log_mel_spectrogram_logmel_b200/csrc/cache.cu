@@ -27,6 +27,7 @@ struct logmel_cache_plan {
   int* d_status = nullptr;
   int* d_tickets = nullptr;   // split rows: one counter per worker, zero between calls
   float* d_parts = nullptr;   // split rows: two partial tiles per worker
+  SplitItem* d_splits = nullptr;   // split items of the chunk kernel, one per CTA
 };
 
 namespace {
@@ -289,7 +290,11 @@ logmel_status launch_attend(const logmel_cache_plan* p, const AttendArgs& a, int
         !encode_pages(p, &x.k_map, c.k, c.n_pages, c.k_page, c.k_head, c.k_slot, x.box_keys) ||
         !encode_pages(p, &x.v_map, c.v, c.n_pages, c.v_page, c.v_head, c.v_slot, x.box_keys))
       return no_map(__LINE__);
+    x.splits = p->d_splits;
     attend_chunk_kernel<T, D><<<p->sms, CHUNK_THREADS, ChunkShape<D>::SMEM, str>>>(x);
+    const logmel_status st = launched(__LINE__);
+    if (st != LOGMEL_OK) return st;
+    join_kernel<T, D><<<dim3(p->sms, ITEM_ROWS / JOIN_ROWS), JOIN_THREADS, 0, str>>>(x);
   }
   return launched(__LINE__);
 }
@@ -302,7 +307,7 @@ logmel_status launch_weigh_columns(const logmel_cache_plan* p, WeighArgs& a, cud
   if (!encode_rows(p, &a.q_map, a.q, a.b.rows, a.n_q, a.tokens) ||
       !encode_pages(p, &a.k_map, c.k, c.n_pages, c.k_page, c.k_head, c.k_slot, a.box_keys))
     return no_map(__LINE__);
-  weigh_kernel<T, D, N><<<p->sms, CHUNK_THREADS, WeighShape<D, N>::SMEM, str>>>(a);
+  weigh_kernel<T, D, N><<<p->sms, WeighShape<D, N>::THREADS, WeighShape<D, N>::SMEM, str>>>(a);
   return launched(__LINE__);
 }
 
@@ -352,7 +357,8 @@ logmel_status logmel_cache_plan_create(const logmel_cache_config* config, logmel
   if (!tensor_map_encoder()) return fail(record_cuda_error(cudaErrorNotSupported, "cuTensorMapEncodeTiled", "cache.cu", __LINE__));
   const size_t tickets = sizeof(int) * (size_t)p->sms * ROWS_CTAS * ROWS_WARPS;
   if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess || cudaMalloc(&p->d_tickets, tickets) != cudaSuccess ||
-      cudaMalloc(&p->d_parts, parts_bytes(p)) != cudaSuccess) {
+      cudaMalloc(&p->d_parts, parts_bytes(p)) != cudaSuccess ||
+      cudaMalloc(&p->d_splits, sizeof(SplitItem) * p->sms) != cudaSuccess) {
     cudaGetLastError();
     return fail(LOGMEL_ERR_OOM);
   }
@@ -376,6 +382,7 @@ void logmel_cache_plan_destroy(logmel_cache_plan* p) {
     cudaFree(p->d_status);
     cudaFree(p->d_tickets);
     cudaFree(p->d_parts);
+    cudaFree(p->d_splits);
   }
   delete p;
 }

@@ -4,7 +4,8 @@
 // query heads of the key head, so that heads which share keys share the loads.  Keys
 // come in units of 128 slots.  All units of the launch form one line (stream,
 // key head, item, unit) that is cut into equal runs, one per CTA; items that
-// fall into several runs are joined by the CTA that finishes last, in order.
+// fall into several runs are joined by join_kernel, in order.  (Joined by the CTA that finished last, one SM had to
+// read all the parts of an item: 18 us for 7 parts.)
 //
 // Roles of a CTA (384 threads):
 //   warps 0-3, 4-7   softmax of tile 0 and of tile 1, one thread per row: scores from
@@ -30,10 +31,15 @@ constexpr int ITEM_ROWS = 2 * TILE_ROWS;
 constexpr int TILE_KEYS = 128;
 constexpr int CHUNK_THREADS = 384;
 constexpr int CHUNK_MIN_UNITS = 2;
+// Starting and ending an item takes as long as about two units, so on the line
+// an item is that much longer (its first two places are no units).  Without it, CTAs
+// of many short items finished last: 16 items, 580,000 clocks against 440,000 for 3 items of as many units.
+constexpr int ITEM_COST = 2;
 constexpr int MAX_CTAS = 160;
 constexpr int WAVES_MAX = 5;        // beyond, the few split items of the one line do not matter
 constexpr float RESCALE_AT = 8.f;   // in powers of two
-constexpr uint32_t FIT_PAIRS = 0x4a94;   // of every 16 pairs of weights, those computed on the FMA pipe
+constexpr uint32_t FIT_PAIRS = 0x2222;   // of every 16 pairs of weights, those computed on the FMA pipe (4: 290 us for a
+                                         // prompt of 8,192 tokens against 300 for none and 298 for 8)
 
 template <int D>
 struct ChunkShape {
@@ -44,8 +50,15 @@ struct ChunkShape {
   static constexpr int O_COLUMN = 256;                        // accumulators at 256 and 384, scores at 0 and 128
 };
 
+// An item that begins in a CTA's run and ends in a later one's.
+struct SplitItem {
+  int last;               // the CTA it ends in, or -1: there is none
+  int s, h, i0, count;
+};
+
 struct ChunkArgs : AttendArgs {
   CUtensorMap q_map, k_map, v_map;
+  SplitItem* splits;   // one per CTA
   int tokens;      // tokens of a tile: 128 / group
   int box_keys;    // slots a key copy brings: min(page size, 128)
 };
@@ -56,6 +69,7 @@ struct Item {
   int lo, hi;             // seen by some row
   int2 first, last;       // seen by the first and by the last token
   int begin, units;       // in units of 128 slots
+  __device__ int cost() const { return units + ITEM_COST; }
 };
 
 __device__ __forceinline__ Item item_of(const ChunkArgs& a, int n, int len, int qt) {
@@ -111,19 +125,57 @@ __device__ __forceinline__ ChunkPlace place_of_item(const ChunkArgs& a, int i) {
   return p;
 }
 
-// Walks the CTA's segments (runs of units of one item): its whole items, then its run [u0, u1) from `p` on.
-template <typename F>
-__device__ __forceinline__ void for_segments(const ChunkArgs& a, int waves, ChunkPlace p, int64_t u0, int64_t u1, F&& f) {
+// A run of units [t0, t1) of one item, and where the item begins on the line.
+struct Segment {
+  ChunkPlace p;
+  int t0, t1, number;   // number < 0: no more
+  int64_t item_begin;
+};
+
+// The CTA's segments: its whole items, then its run [u, u1) of the line from `p` on.
+struct Walk {
+  const ChunkArgs& a;
+  int waves;
+  ChunkPlace p;
+  int64_t u, u1;
   int seg = 0;
-  for (; seg < waves; ++seg) {
-    const ChunkPlace w = place_of_item(a, seg * gridDim.x + blockIdx.x);
-    if (!f(w, seg, 0, w.x.units, (int64_t)0)) return;
+
+  __device__ Segment next() {
+    Segment s;
+    if (seg < waves) {
+      s.p = place_of_item(a, seg * gridDim.x + blockIdx.x);
+      s.t0 = 0;
+      s.t1 = s.p.x.units;
+      s.item_begin = 0;
+      s.number = seg++;
+      return s;
+    }
+    while (u < u1) {
+      const int c0 = p.unit, c1 = (int)min((int64_t)p.x.cost(), p.unit + (u1 - u));
+      s.p = p;
+      s.t0 = max(0, c0 - ITEM_COST);
+      s.t1 = max(0, c1 - ITEM_COST);
+      s.item_begin = u - c0;
+      u += c1 - c0;
+      if (u < u1) p.next_item(a);
+      if (s.t1 > s.t0) {
+        s.number = seg++;
+        return s;
+      }
+    }
+    s.number = -1;
+    return s;
   }
-  for (int64_t u = u0; u < u1; ++seg) {
-    const int t0 = p.unit, t1 = (int)min((int64_t)p.x.units, p.unit + (u1 - u));
-    if (!f(p, seg, t0, t1, u - t0)) return;
-    u += t1 - t0;
-    if (u < u1) p.next_item(a);
+};
+
+// f(place, number, t0, t1, begin of the item, ahead): f calls `ahead` where it has time to work out the next segment.
+template <typename F>
+__device__ __forceinline__ void for_segments(const ChunkArgs& a, int waves, const ChunkPlace& p, int64_t u0, int64_t u1, F&& f) {
+  Walk walk{a, waves, p, u0, u1};
+  Segment s = walk.next(), after;
+  while (s.number >= 0) {
+    if (!f(s.p, s.number, s.t0, s.t1, s.item_begin, [&] { after = walk.next(); })) return;
+    s = after;
   }
 }
 
@@ -132,9 +184,9 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
   using Shape = ChunkShape<D>;
   constexpr int STAGES = Shape::STAGES, TILE = Shape::TILE, HALVES = D / 64, HALF_TILE = TILE / HALVES;
   extern __shared__ char smem_raw[];
-  __shared__ alignas(8) uint64_t bars[10 + 3 * STAGES];
+  __shared__ alignas(8) uint64_t bars[8 + 3 * STAGES];
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int stop_sh, ticket_sh;
+  __shared__ int stop_sh;
   __shared__ int poison[16];
   __shared__ int64_t warp_total[CHUNK_THREADS / 32];
   __shared__ ChunkPlace start_sh;
@@ -152,8 +204,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
   auto empty = [&](int i) { return bar0 + 8 * (2 + 2 * STAGES + i); };
   auto s_full = [&](int i) { return bar0 + 8 * (2 + 3 * STAGES + i); };
   auto p_full = [&](int i) { return bar0 + 8 * (4 + 3 * STAGES + i); };
-  const uint32_t joined = bar0 + 8 * (6 + 3 * STAGES), counted = bar0 + 8 * (7 + 3 * STAGES);
-  auto o_seen = [&](int i) { return bar0 + 8 * (8 + 3 * STAGES + i); };
+  auto o_full = [&](int i) { return bar0 + 8 * (6 + 3 * STAGES + i); };
 
   if (warp == 9) tmem_alloc(smem_address(&tmem_base_sh), 512);
   if (tid == 0) {
@@ -167,11 +218,13 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), 4);
-      mbar_init(o_seen(i), 4);
+      mbar_init(o_full(i), 1);
     }
-    mbar_init(joined, 8);
-    mbar_init(counted, 1);
     stop_sh = 0;
+    a.splits[blockIdx.x].last = -1;
+    prefetch_map(&a.q_map);
+    prefetch_map(&a.k_map);
+    prefetch_map(&a.v_map);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid < 16) poison[tid] = -1;
@@ -186,7 +239,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
       if (n > 4 * item_tokens) continue;
       const int len = a.c.length(s, blockIdx.x == 0);
       int64_t sum = 0;
-      for (int qt = 0; qt * item_tokens < n; ++qt) sum += item_of(a, n, len, qt).units;
+      for (int qt = 0; qt * item_tokens < n; ++qt) sum += item_of(a, n, len, qt).cost();
       before[s] = sum;
     }
     for (int s = warp; s < S; s += CHUNK_THREADS / 32) {
@@ -194,7 +247,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
       if (n <= 4 * item_tokens) continue;
       const int len = a.c.length(s, blockIdx.x == 0 && lane == 0);
       int64_t all = 0;
-      for (int qt = lane; qt * item_tokens < n; qt += 32) all += item_of(a, n, len, qt).units;
+      for (int qt = lane; qt * item_tokens < n; qt += 32) all += item_of(a, n, len, qt).cost();
       for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(~0u, all, d);
       if (lane == 0) before[s] = all;
     }
@@ -225,7 +278,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
     __syncthreads();
   }
   const int64_t total = before[S] * a.n_kv;
-  const int64_t quota = max((int64_t)CHUNK_MIN_UNITS, (total + gridDim.x - 1) / gridDim.x);
+  const int64_t quota = max((int64_t)CHUNK_MIN_UNITS + ITEM_COST, (total + gridDim.x - 1) / gridDim.x);
 
   // Where all streams push the same and there are some whole items for every
   // CTA, these go first, one per CTA at a time in the order of the line: CTAs of the
@@ -245,7 +298,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
     bool over = false;
     if (tid < G) {
       int64_t own = 0;
-      for (int w = 0; w < waves; ++w) own += place_of_item(a, w * G + tid).x.units;
+      for (int w = 0; w < waves; ++w) own += place_of_item(a, w * G + tid).x.cost();
       over = own > quota;
       bound[tid + 1] = (int)(quota - own);   // room left; below 2^31: a length is
     }
@@ -284,14 +337,14 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
       int i = waves * G;
       for (; i < n_items; ++i) {
         p = place_of_item(a, i);
-        if (left < p.x.units) break;
-        left -= p.x.units;
+        if (left < p.x.cost()) break;
+        left -= p.x.cost();
       }
       // the last runs may reach past the last item
       int64_t end = 0;
       if (i < n_items) {
         end = u0 - left;
-        for (int j = i; j < n_items && end < u1; ++j) end += place_of_item(a, j).x.units;
+        for (int j = i; j < n_items && end < u1; ++j) end += place_of_item(a, j).x.cost();
       }
       run_end_sh = min(u1, max(u0, end));
       if (i == n_items) run_end_sh = u0;
@@ -310,8 +363,8 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
       left -= p.h * per_head;
       p.qt = 0;
       p.x = item_of(a, p.n, p.len, 0);
-      while (left >= p.x.units) {
-        left -= p.x.units;
+      while (left >= p.x.cost()) {
+        left -= p.x.cost();
         p.x = item_of(a, p.n, p.len, ++p.qt);
       }
       run_end_sh = u1;
@@ -346,17 +399,21 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
       const int in_page = (1 << a.c.page_shift) - 1;
       const int boxes = TILE_KEYS / a.box_keys;                  // per tile and 64 columns
       const uint32_t box_bytes = a.box_keys * 128;
-      for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int, int t0, int t1, int64_t) {
-        if (q_uses > 0 && !mbar_wait(q_free, (q_uses - 1) & 1, stop, status)) return false;
-        ++q_uses;
+      for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int, int t0, int t1, int64_t, auto&& ahead) {
         const int tiles = p.x.count > a.tokens ? 2 : 1;
-        if (lane == 0) {
-          const int row = a.b.begin(p.s) + p.x.i0;
-          mbar_expect(q_full, tiles * HALVES * a.tokens * a.group * 128);
-          for (int i = 0; i < tiles; ++i)
-            for (int c = 0; c < HALVES; ++c)
-              tma_load_3d(q_smem + i * TILE + c * HALF_TILE, &a.q_map, 64 * c, p.h * a.group, row + i * a.tokens, q_full);
-        }
+        auto load_queries = [&] {
+          if (q_uses > 0 && !mbar_wait(q_free, (q_uses - 1) & 1, stop, status)) return false;
+          ++q_uses;
+          if (lane == 0) {
+            const int row = a.b.begin(p.s) + p.x.i0;
+            mbar_expect(q_full, tiles * HALVES * a.tokens * a.group * 128);
+            for (int i = 0; i < tiles; ++i)
+              for (int c = 0; c < HALVES; ++c)
+                tma_load_3d(q_smem + i * TILE + c * HALF_TILE, &a.q_map, 64 * c, p.h * a.group, row + i * a.tokens, q_full);
+          }
+          __syncwarp();
+          return true;
+        };
         // lane -> (box, 64-column half); boxes without a seen slot are left out
         const int box = lane / HALVES, half = lane % HALVES;
         auto page_of = [&](int t) {
@@ -379,15 +436,18 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
               tma_load_4d(ring + stage * TILE + half * HALF_TILE + box * box_bytes, kv ? &a.v_map : &a.k_map, 64 * half,
                           key & in_page, p.h, page, full(stage));
             if (++stage == STAGES) stage = 0, phase ^= 1;
+            // the first keys need not wait until the last item's queries are done with
+            if (t == t0 && kv == 0 && !load_queries()) return false;
           }
         }
+        ahead();
         return true;
       });
     } else if (warp == 9) {
       // ---- products ----
       int stage = 0;          // of the next tile in the ring
       uint32_t phase = 0, q_phase = 0;
-      uint32_t p_phase[2] = {0, 0}, o_phase[2] = {1, 1};
+      uint32_t p_phase[2] = {0, 0};
       constexpr uint32_t KIND_S = mma_kind<T>(TILE_ROWS, TILE_KEYS, false), KIND_O = mma_kind<T>(TILE_ROWS, D, true);
       auto next = [&] {
         if (++stage == STAGES) stage = 0, phase ^= 1;
@@ -410,29 +470,30 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
                    add || j > 0);
         }
       };
-      for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int, int t0, int t1, int64_t) {
+      for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int, int t0, int t1, int64_t, auto&& ahead) {
         const int tiles = p.x.count > a.tokens ? 2 : 1;
         if (!mbar_wait(q_full, q_phase, stop, status)) return false;
         q_phase ^= 1;
         int k_stage = stage;
-        if (!mbar_wait(full(k_stage), phase, stop, status)) return false;
+        if (!mbar_wait(clean(k_stage), phase, stop, status)) return false;
         next();
         tmem_fence_after();
-        for (int i = 0; i < tiles; ++i) {
-          // the softmax has to have seen the end of the tile's last item: two unseen phases would look like none
-          if (!mbar_wait(o_seen(i), o_phase[i], stop, status)) return false;
-          o_phase[i] ^= 1;
-          scores(i, ring + k_stage * TILE);
+        // the scores go over weights that the products issued last still read: MMAs run in order
+        for (int i = 0; i < tiles; ++i) scores(i, ring + k_stage * TILE);
+        if (elect_lane()) {
+          mma_commit(empty(k_stage));
+          if (t0 + 1 == t1) mma_commit(q_free);
         }
-        if (elect_lane()) mma_commit(empty(k_stage));
+        __syncwarp();
+        ahead();   // while the first softmax runs
         for (int t = t0; t < t1; ++t) {
           const int v_stage = stage;
-          if (!mbar_wait(clean(v_stage), phase, stop, status) || !mbar_wait(full(v_stage), phase, stop, status)) return false;
+          if (!mbar_wait(clean(v_stage), phase, stop, status)) return false;
           next();
           const bool more = t + 1 < t1;
           if (more) {
             k_stage = stage;
-            if (!mbar_wait(full(k_stage), phase, stop, status)) return false;
+            if (!mbar_wait(clean(k_stage), phase, stop, status)) return false;
             next();
           }
           for (int i = 0; i < tiles; ++i) {
@@ -441,12 +502,12 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
             tmem_fence_after();
             values(i, ring + v_stage * TILE, t > t0);
             if (more) scores(i, ring + k_stage * TILE);           // after the weights that it overwrites were read
-            else if (elect_lane()) mma_commit(s_full(i));            // the accumulator is complete
+            else if (elect_lane()) mma_commit(o_full(i));
           }
           if (elect_lane()) {
             mma_commit(empty(v_stage));
             if (more) mma_commit(empty(k_stage));
-            else mma_commit(q_free);
+            if (t + 2 == t1) mma_commit(q_free);   // the item's last scores are under way
           }
           __syncwarp();
         }
@@ -460,54 +521,65 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
         if (++stage == STAGES) stage = 0, phase ^= 1;
       };
       const int id = tid - 320;
-      for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int seg, int t0, int t1, int64_t) {
+      for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int seg, int t0, int t1, int64_t, auto&& ahead) {
         for (int t = t0; t < t1; ++t) {
-          // keys need no cleaning, but their stage's phase moves on all the same, no sooner than they are there:
-          // an arrival ahead of the products could pass the phase that they still have to see
+          // Keys need no cleaning, but pass through here like the values: the products wait for `clean` of every stage, so
+          // that no stage can be filled twice before this warp has seen it once.
           if (!mbar_wait(full(stage), phase, stop, status)) return false;
           if (lane == 0) mbar_arrive(clean(stage));
           next();
           if (!mbar_wait(full(stage), phase, stop, status)) return false;
+          // rows of the tile: [0, dead_lo) and [dead_hi, 128) are seen by none; [dead_lo, some_lo) and
+          // [some_hi, dead_hi) by some; the rest by all
           const int key0 = (p.x.begin + t) * TILE_KEYS;
-          const int dead_lo = p.x.lo - key0, dead_hi = p.x.hi - key0;
-          const bool some_dead = dead_lo > 0 || dead_hi < TILE_KEYS;
-          // seen by some rows only
-          const bool mixed = (key0 < p.x.last.x && key0 + TILE_KEYS > p.x.first.x) ||
-                             (key0 < p.x.last.y && key0 + TILE_KEYS > p.x.first.y);
-          if (some_dead || mixed) {
-            bool bad = false;
-            for (int c = id; c < TILE_KEYS * D / 8; c += 64) {     // 16-byte pieces
-              const int r = (c >> 3) & (TILE_KEYS - 1), key = key0 + r;
-              const uint32_t at = ring + stage * TILE + c * 16;
-              if (r < dead_lo || r >= dead_hi) {
-                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
-              } else if ((key < p.x.last.x) || (key >= p.x.first.y)) {
-                uint32_t w[4];
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
-                uint32_t keep = 0xffffffffu;
-                constexpr uint32_t E = Half2<T>::EXPONENT;
+          auto row_of = [&](int key) { return min(max(key - key0, 0), TILE_KEYS); };
+          const int dead_lo = row_of(p.x.lo), dead_hi = max(row_of(p.x.hi), dead_lo);
+          const int some_lo = min(max(row_of(p.x.last.x), dead_lo), dead_hi);
+          const int some_hi = max(min(row_of(p.x.first.y), dead_hi), some_lo);
+          const uint32_t tile = ring + stage * TILE;
+          auto piece = [&](int r0, int i) {   // 16 bytes: piece i of the rows from r0 on (the swizzle stays within a row)
+            return tile + (i % (D / 8) >> 3) * HALF_TILE + (r0 + i / (D / 8)) * 128 + (i & 7) * 16;
+          };
+          auto zero = [&](int r0, int r1) {
+            for (int i = id; i < (r1 - r0) * (D / 8); i += 64)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(piece(r0, i)), "r"(0) : "memory");
+          };
+          auto clean_rows = [&](int r0, int r1) {
+            const int n = (r1 - r0) * (D / 8);
+            uint32_t acc = 0;
+#pragma unroll 4
+            for (int i = id; i < n; i += 64) {
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(piece(r0, i)) : "memory");
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  uint32_t k = 0xffffffffu;
-                  if ((w[e] & E & 0xffffu) == (E & 0xffffu)) k &= 0xffff0000u;
-                  if ((w[e] & E & 0xffff0000u) == (E & 0xffff0000u)) k &= 0xffffu;
-                  w[e] &= k;
-                  keep &= k;
-                }
-                if (keep != 0xffffffffu) {
-                  bad = true;
-                  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-                }
-              }
+              for (int e = 0; e < 4; ++e) acc = Half2<T>::times_zero(w[e], acc);
             }
-            if (bad) *(volatile int*)&poison[seg & 15] = seg;
-            fence_async_smem();
-          }
+            if ((acc & 0x7fff7fffu) == 0) return;   // all finite
+            *(volatile int*)&poison[seg & 15] = seg;
+            for (int i = id; i < n; i += 64) {
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(piece(r0, i)) : "memory");
+              constexpr uint32_t E = Half2<T>::EXPONENT;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((w[e] & E & 0xffffu) == (E & 0xffffu)) w[e] &= 0xffff0000u;
+                if ((w[e] & E & 0xffff0000u) == (E & 0xffff0000u)) w[e] &= 0xffffu;
+              }
+              asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(piece(r0, i)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+            }
+          };
+          zero(0, dead_lo);
+          zero(dead_hi, TILE_KEYS);
+          clean_rows(dead_lo, some_lo);
+          clean_rows(some_hi, dead_hi);
+          fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(clean(stage));
           next();
         }
+        ahead();
         return true;
       });
     }
@@ -518,10 +590,12 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);   // this warp's 32 lanes
     const uint32_t s_tmem = lanes + 128 * tile, o_tmem = lanes + Shape::O_COLUMN + 128 * tile;
     const float sc = a.scale * LOG2E;
-    uint32_t s_phase = 0, join_phase = 0;
-    for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int seg, int t0, int t1, int64_t item_begin) {
+    const int tok = row / a.group;
+    uint32_t s_phase = 0, o_phase = 0;
+    for_segments(a, waves, start, u0, u1, [&](const ChunkPlace& p, int seg, int t0, int t1, int64_t item_begin, auto&& ahead) {
+      ahead();
       const bool whole = t0 == 0 && t1 == p.x.units;
-      const int tok = row / a.group, count = p.x.count - tile * a.tokens;   // tokens of this tile
+      const int count = p.x.count - tile * a.tokens;   // tokens of this tile
       const bool valid = tok < min(count, a.tokens);
       const int i = p.x.i0 + tile * a.tokens + tok;                         // token in the push
       const int2 mine = valid ? seen(p.len, p.n, i, a.causal, a.window) : make_int2(0, 0);
@@ -535,23 +609,43 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
           if (!mbar_wait(s_full(tile), s_phase, stop, status)) return false;
           s_phase ^= 1;
           tmem_fence_after();
-          uint32_t x[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_load32(x + 32 * c, s_tmem + 32 * c);
-          tmem_wait_load();
+          // Two passes over the scores in tensor memory (maximum, then weights), 32 columns at a time with the next 32 on
+          // their way: the loops stay short enough for the instruction cache, and 128 scores a thread out of the registers.
           bool plain = key0 >= all_lo && key0 + TILE_KEYS <= all_hi;   // every row sees every key
-          if (!plain) {
-            const int lo = mine.x - key0, hi = mine.y - key0;
+          const int lo = mine.x - key0, hi = mine.y - key0;
+          auto in_turn = [&](auto&& f) {
+            uint32_t x0[32], x1[32];
+            tmem_load32(x0, s_tmem);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 64) {
+              tmem_wait_load();
+              tmem_load32(x1, s_tmem + c + 32);
+              f(x0, c);
+              tmem_wait_load();
+              if (c == 0) tmem_load32(x0, s_tmem + 64);
+              f(x1, c + 32);
+            }
+          };
+          auto mask = [&](uint32_t* x, int c) {   // a bit per column, so that an element costs one test
+            const int l0 = min(max(lo - c, 0), 32), h0 = min(max(hi - c, 0), 32);
+            const uint32_t bits = (uint32_t)((1ull << h0) - 1) & ~(uint32_t)((1ull << l0) - 1);
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c < lo || c >= hi) x[c] = 0xff800000u;
-          }
+            for (int e = 0; e < 32; ++e)
+              if (!(bits >> e & 1)) x[e] = 0xff800000u;
+          };
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto take_max = [&](const uint32_t* x) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              top[e] = max3_nan(top[e], __uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
+            for (int e = 0; e < 32; e += 2) top[e / 2 & 3] = max3_nan(top[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          };
+          if (plain) {
+            in_turn([&](uint32_t* x, int) { take_max(x); });
+          } else {
+            in_turn([&](uint32_t* x, int c) {
+              mask(x, c);
+              take_max(x);
+            });
+          }
           // rows past the item's hold whatever the tile holds there: they must not choose the warp's path
           const float high = valid ? max3_nan(max3_nan(top[0], top[1], top[2]), top[3], top[3]) * sc : -INFINITY;
           const bool grow = !(high <= m + RESCALE_AT);   // also where high is NaN
@@ -563,7 +657,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
             }
             plain = plain && !__any_sync(~0u, !(high < INFINITY));
             if (t > t0) {   // the product before this one is complete: its scores came after it
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D; c += 16) {
                 uint32_t o[16];
                 tmem_load16(o, o_tmem + c);
@@ -576,15 +670,14 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
           }
           const float use = m == -INFINITY ? 0.f : m;
           const uint64_t sc2 = pack2(sc, sc), use2 = pack2(-use, -use);
-          uint64_t sum = pack2(0.f, 0.f);
-          // sums before the weights are rounded to the rows' type
+          uint64_t sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+          // sums before the weights are rounded to the rows' type; a weight's columns lie over scores already read
           if (plain) {
-#pragma unroll
-            for (int c = 0; c < 128; c += 32) {
+            in_turn([&](uint32_t* x, int c) {
               uint32_t w[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const uint64_t y = fma2(pack2(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), sc2, use2);
+                const uint64_t y = fma2(pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, use2);
                 float2 pw;
                 if (FIT_PAIRS >> e & 1) {
                   pw = unpack2(exp2_fit(y));
@@ -592,35 +685,34 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
                   const float2 z = unpack2(y);
                   pw = make_float2(exp2_approx(z.x), exp2_approx(z.y));
                 }
-                sum = add2(sum, pack2(pw.x, pw.y));
+                sum[e & 1] = add2(sum[e & 1], pack2(pw.x, pw.y));
                 w[e] = Half2<T>::from_float(pw.x, pw.y);
               }
               tmem_store16(s_tmem + c / 2, w);
-            }
+            });
           } else {
-#pragma unroll
-            for (int c = 0; c < 128; c += 32) {
+            in_turn([&](uint32_t* x, int c) {
+              mask(x, c);
               uint32_t w[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const float p0 = exp2_approx(fmaf(__uint_as_float(x[c + 2 * e]), sc, -use));
-                const float p1 = exp2_approx(fmaf(__uint_as_float(x[c + 2 * e + 1]), sc, -use));
-                sum = add2(sum, pack2(p0, p1));
+                const float p0 = exp2_approx(fmaf(__uint_as_float(x[2 * e]), sc, -use));
+                const float p1 = exp2_approx(fmaf(__uint_as_float(x[2 * e + 1]), sc, -use));
+                sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
                 w[e] = Half2<T>::from_float(p0, p1);
               }
               tmem_store16(s_tmem + c / 2, w);
-            }
+            });
           }
           tmem_wait_store();
           tmem_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full(tile));
-          const float2 both = unpack2(sum);
+          const float2 both = unpack2(add2(sum[0], sum[1]));
           l += both.x + both.y;
         }
-        if (!mbar_wait(s_full(tile), s_phase, stop, status)) return false;   // the accumulator is complete
-        s_phase ^= 1;
-        if (lane == 0) mbar_arrive(o_seen(tile));
+        if (!mbar_wait(o_full(tile), o_phase, stop, status)) return false;   // the accumulator is complete
+        o_phase ^= 1;
         tmem_fence_after();
       }
       // values that were taken out, for the rows that see them
@@ -646,23 +738,49 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
       if (whole) {
         if (count > 0) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          T* out = (T*)a.out.data + t_row * a.out.row + (int64_t)hq * a.out.head;
+          // A thread holds a row.  Four lanes exchange 16-byte pieces of 32 columns so that each store instruction writes 64
+          // consecutive bytes of 8 rows: stored row by thread, 32 rows an instruction, the lines of one item held up
+          // the barriers' shared-memory traffic for 6,000 clocks.
+          const int quad = lane & 3;
+          int64_t to[4];   // the rows of the four lanes
+          {
+            const int64_t mine_at = valid ? t_row * a.out.row + (int64_t)hq * a.out.head : -1;
 #pragma unroll
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_load16(o, o_tmem + c);
+            for (int e = 0; e < 4; ++e) to[e] = __shfl_sync(~0u, mine_at, (lane & ~3) + e);
+          }
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_load32(o, o_tmem + c);
             tmem_wait_load();
-            float y[16];
+            float y[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
-            if (fix) add_taken_out(y, c);
-            if (valid) {
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = Half2<T>::from_float(y[2 * e], y[2 * e + 1]);
-              *(uint4*)(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
-              *(uint4*)(out + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            for (int e = 0; e < 32; ++e) y[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+            if (fix) {
+              add_taken_out(y, c);
+              add_taken_out(y + 16, c + 16);
             }
+            uint32_t w[4][4];   // [piece][word]; after the exchange [row of the quad][word] of piece `quad`
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e >> 2][e & 3] = Half2<T>::from_float(y[2 * e], y[2 * e + 1]);
+#pragma unroll
+            for (int bit = 1; bit < 4; bit <<= 1) {
+              const bool upper = lane & bit;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!(e & bit)) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t give = upper ? w[e][k] : w[e | bit][k];
+                    const uint32_t got = __shfl_xor_sync(~0u, give, bit);
+                    if (upper) w[e][k] = got;
+                    else w[e | bit][k] = got;
+                  }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (to[e] >= 0) *(uint4*)((T*)a.out.data + to[e] + c + 8 * quad) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
           }
           if (valid && a.lse) a.lse[t_row * a.n_q + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
         }
@@ -694,52 +812,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
           }
         }
       }
-      __threadfence();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(joined);
-      const int first = owner(item_begin), last = owner(item_begin + p.x.units - 1);
-      if (tid == 0 && mbar_wait_thread(joined, join_phase, stop, status)) {
-        const int done = atomicAdd(a.tickets + first, 1);
-        if (done == last - first) a.tickets[first] = 0;   // ready for the next call
-        ticket_sh = done;
-        mbar_arrive(counted);
-      }
-      __syncwarp();
-      if (!mbar_wait(counted, join_phase, stop, status)) return false;
-      join_phase ^= 1;
-      if (*(volatile int*)&ticket_sh == last - first) {
-        __threadfence();
-        auto slot = [&](int w) { return a.parts + (int64_t)(2 * w + (w == first ? 1 : 0)) * Shape::PART; };
-        const int rows = p.x.count > a.tokens ? ITEM_ROWS : TILE_ROWS;
-        for (int u = tid; u < rows * (D / 4); u += 256) {   // a thread keeps to one row: 256 is a multiple of the rows
-          const int r = u % rows, d4 = u / rows;
-          const int tk = (r & 127) / a.group, j = (r >> 7) * a.tokens + tk;
-          if (tk >= a.tokens || j >= p.x.count) continue;
-          float mm = -INFINITY;
-          for (int w = first; w <= last; ++w) mm = fmaxf(mm, __ldcg(slot(w) + r));
-          const float base = mm == -INFINITY ? 0.f : mm;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float sum = 0.f;
-#pragma unroll 4
-          for (int w = first; w <= last; ++w) {
-            const float* sl = slot(w);
-            const float f = exp2_approx(__ldcg(sl + r) - base);
-            const float4 y = __ldcg((const float4*)(sl + 2 * ITEM_ROWS) + d4 * ITEM_ROWS + r);
-            sum += f * __ldcg(sl + ITEM_ROWS + r);
-            acc.x += f * y.x;
-            acc.y += f * y.y;
-            acc.z += f * y.z;
-            acc.w += f * y.w;
-          }
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          const int64_t tr = a.b.begin(p.s) + p.x.i0 + j;
-          const int head = p.h * a.group + (r & 127) - tk * a.group;
-          uint2 w = make_uint2(Half2<T>::from_float(acc.x * inv, acc.y * inv), Half2<T>::from_float(acc.z * inv, acc.w * inv));
-          if (sum == 0.f) w = make_uint2(0u, 0u);
-          *(uint2*)((T*)a.out.data + tr * a.out.row + (int64_t)head * a.out.head + 4 * d4) = w;
-          if (a.lse && d4 == 0) a.lse[tr * a.n_q + head] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * LN2;
-        }
-      }
+      if (t0 == 0 && tid == 0) a.splits[blockIdx.x] = SplitItem{owner(item_begin + p.x.cost() - 1), p.s, p.h, p.x.i0, p.x.count};
       return true;
     });
   }
@@ -749,6 +822,57 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
   tmem_fence_before();
   __syncthreads();
   if (warp == 9) tmem_free(tmem, 512);
+}
+
+// Joins the parts of split items: CTA (w, i) takes 32 rows of the item that
+// begins in run w, a lane per row and D / 8 columns per warp.
+constexpr int JOIN_ROWS = 32;
+constexpr int JOIN_THREADS = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ ChunkArgs a) {
+  constexpr int PART = ChunkShape<D>::PART, PIECES = D / 32;   // pieces of 4 columns per warp
+  const int first = blockIdx.x;
+  const SplitItem x = a.splits[first];
+  const int r = blockIdx.y * JOIN_ROWS + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+  const int tk = (r & 127) / a.group, j = (r >> 7) * a.tokens + tk;
+  if (x.last < 0 || tk >= a.tokens || j >= x.count) return;
+  auto slot = [&](int w) { return a.parts + (int64_t)(2 * w + (w == first ? 1 : 0)) * PART; };
+  float mm = -INFINITY;
+#pragma unroll 4
+  for (int w = first; w <= x.last; ++w) mm = fmaxf(mm, __ldcg(slot(w) + r));
+  const float base = mm == -INFINITY ? 0.f : mm;
+  float4 acc[PIECES];
+  float sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < PIECES; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int w = first; w <= x.last; ++w) {
+    const float* sl = slot(w);
+    const float f = exp2_approx(__ldcg(sl + r) - base);
+    sum += f * __ldcg(sl + ITEM_ROWS + r);
+#pragma unroll
+    for (int e = 0; e < PIECES; ++e) {
+      const float4 y = __ldcg((const float4*)(sl + 2 * ITEM_ROWS) + (PIECES * warp + e) * ITEM_ROWS + r);
+      acc[e].x += f * y.x;
+      acc[e].y += f * y.y;
+      acc[e].z += f * y.z;
+      acc[e].w += f * y.w;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t tr = a.b.begin(x.s) + x.i0 + j;
+  const int head = x.h * a.group + (r & 127) - tk * a.group;
+  T* out = (T*)a.out.data + tr * a.out.row + (int64_t)head * a.out.head + 4 * PIECES * warp;
+#pragma unroll
+  for (int e = 0; e < PIECES; e += 2) {
+    uint4 w = make_uint4(Half2<T>::from_float(acc[e].x * inv, acc[e].y * inv), Half2<T>::from_float(acc[e].z * inv, acc[e].w * inv),
+                         Half2<T>::from_float(acc[e + 1].x * inv, acc[e + 1].y * inv),
+                         Half2<T>::from_float(acc[e + 1].z * inv, acc[e + 1].w * inv));
+    if (sum == 0.f) w = make_uint4(0u, 0u, 0u, 0u);
+    *(uint4*)(out + 4 * e) = w;
+  }
+  if (a.lse && warp == 0) a.lse[tr * a.n_q + head] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * LN2;
 }
 
 }  // namespace cache

@@ -100,6 +100,11 @@ struct Half2<__nv_bfloat16> {
     return r;
   }
   static constexpr uint32_t EXPONENT = 0x7f807f80u;   // both halves' exponent bits
+  // acc + 0 * x: turns (and stays) NaN where x is not finite
+  static __device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t acc) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    return acc;
+  }
 };
 template <>
 struct Half2<__half> {
@@ -112,6 +117,10 @@ struct Half2<__half> {
     return r;
   }
   static constexpr uint32_t EXPONENT = 0x7c007c00u;
+  static __device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t acc) {
+    asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    return acc;
+  }
 };
 
 }  // namespace cache

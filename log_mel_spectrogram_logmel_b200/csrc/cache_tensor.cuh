@@ -77,6 +77,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // One lane of a converged warp, always the same.  (The MMA's operands live in
@@ -193,6 +196,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
+  const float2 y = unpack2(x);
+  return pack2(exp2_approx(y.x), exp2_approx(y.y));
 }
 
 // 2^x of two values on the FMA pipe, for finite x <= 100 or so; below -126

@@ -13,9 +13,14 @@
 // them; N = 128 the others, bound by the exponentials (one per pair of row
 // and key against 2 x head_dim tensor-core operations).
 //
-// Roles as in the attention kernel: warps 0-3 and 4-7 own one key tile each,
-// warp 8 copies, warp 9 issues the MMAs into two score buffers per tile.
+// Roles: the weight warps (8, or with N = 128 16 of which two share a key and
+// take half of the columns each: two warps a scheduler wait too long on their own
+// results), then one warp that copies queries, one that issues the MMAs into
+// two score buffers per tile, and two that copy keys, half of a tile's copies each (with
+// pages of 16 slots a tile is 16 copies, more than one warp issues in time).
 #pragma once
+#include <type_traits>
+
 #include "cache_chunk.cuh"
 
 namespace logmel {
@@ -41,9 +46,16 @@ struct WeighShape {
   static constexpr int K_STAGES = N == 128 ? 3 : 6, Q_STAGES = N == 128 ? 3 : 4;
   static constexpr int SMEM = 1024 + K_STAGES * K_TILE + Q_STAGES * Q_TILE;
   static constexpr int COLUMNS = N == 128 ? 512 : 64;   // tensor memory: two score buffers per tile
+  static constexpr int HALVES = N == 128 ? 2 : 1;       // weight warps per key
+  static constexpr int WARPS = 8 * HALVES, THREADS = 32 * (WARPS + 4);
+  static constexpr int MY_COLUMNS = N / HALVES;
 };
 
 constexpr int WEIGH_KEYS = 2 * TILE_KEYS;
+#ifndef WFIT
+#define WFIT 0x55
+#endif
+constexpr uint32_t WEIGH_FIT = WFIT;
 
 // Which tokens of a push see some of the slots [k0, k1): [begin, end).
 __device__ __forceinline__ int2 tokens_that_see(const WeighArgs& a, int n, int len, int k0, int k1) {
@@ -78,30 +90,58 @@ struct WeighPlace {
   }
 };
 
-template <typename F>
-__device__ __forceinline__ void for_items(const WeighArgs& a, WeighPlace p, int64_t u, int64_t u1, F&& f) {
-  while (u < u1) {
-    const int k0 = p.item * WEIGH_KEYS, k1 = min(p.len, k0 + WEIGH_KEYS);
-    const int2 tok = tokens_that_see(a, p.n, p.len, k0, k1);
-    if (!f(p, k0, k1, tok, (tok.y - tok.x + a.tokens - 1) / a.tokens)) return;
-    u += p.steps_each(a);
-    if (u < u1 && !p.next(a)) return;
+// An item, the tokens that see some of it, and their steps.
+struct WeighItem {
+  int s, h, k0, k1;     // slots [k0, k1)
+  int n, len;
+  int2 tok;
+  int steps;
+  bool there;
+};
+
+// The items of a CTA: those that begin in [u, u1).
+struct WeighWalk {
+  const WeighArgs& a;
+  WeighPlace p;
+  int64_t u, u1;
+  bool first = true;
+
+  __device__ WeighItem next() {
+    WeighItem x;
+    x.there = false;
+    if (!first) {
+      u += p.steps_each(a);
+      if (u >= u1 || !p.next(a)) u = u1;
+    }
+    first = false;
+    if (u >= u1) return x;
+    x.there = true;
+    x.s = p.s;
+    x.h = p.h;
+    x.n = p.n;
+    x.len = p.len;
+    x.k0 = p.item * WEIGH_KEYS;
+    x.k1 = min(p.len, x.k0 + WEIGH_KEYS);
+    x.tok = tokens_that_see(a, p.n, p.len, x.k0, x.k1);
+    x.steps = (x.tok.y - x.tok.x + a.tokens - 1) / a.tokens;
+    return x;
   }
-}
+};
 
 template <typename T, int D, int N>
-__global__ void __launch_bounds__(CHUNK_THREADS, 1) weigh_kernel(const __grid_constant__ WeighArgs a) {
+__global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(const __grid_constant__ WeighArgs a) {
   using Shape = WeighShape<D, N>;
-  constexpr int KS = Shape::K_STAGES, QS = Shape::Q_STAGES, HALVES = D / 64;
+  constexpr int KS = Shape::K_STAGES, QS = Shape::Q_STAGES, HALVES = D / 64, WARPS = Shape::WARPS, THREADS = Shape::THREADS;
   constexpr int K_HALF = Shape::K_TILE / HALVES, Q_HALF = Shape::Q_TILE / HALVES;
   extern __shared__ char smem_raw[];
-  __shared__ alignas(8) uint64_t bars[2 * KS + 2 * QS + 8];
+  __shared__ alignas(8) uint64_t bars[2 * KS + 2 * QS + 8 + 32];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int stop_sh;
-  __shared__ int64_t warp_total[CHUNK_THREADS / 32];
+  __shared__ int64_t warp_total[THREADS / 32];
   __shared__ WeighPlace start_sh;
   __shared__ int64_t start_u_sh;
-  __shared__ alignas(16) float minus_lse[8][N];
+  __shared__ alignas(16) float minus_lse[WARPS][Shape::MY_COLUMNS];
+  __shared__ float half_sum[4][Shape::HALVES == 2 ? 256 : 1];   // of an item, from the warps of the second half
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* stop = &stop_sh;
   int* status = a.c.status;
@@ -114,11 +154,12 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) weigh_kernel(const __grid_co
   auto q_free = [&](int i) { return bar0 + 8 * (2 * KS + QS + i); };
   auto s_full = [&](int tile, int buf) { return bar0 + 8 * (2 * KS + 2 * QS + 2 * tile + buf); };
   auto s_free = [&](int tile, int buf) { return bar0 + 8 * (2 * KS + 2 * QS + 4 + 2 * tile + buf); };
+  auto half_done = [&](int w, int buf) { return bar0 + 8 * (2 * KS + 2 * QS + 8 + 4 * w + buf); };   // per warp of the first half
 
-  if (warp == 9) tmem_alloc(smem_address(&tmem_base_sh), Shape::COLUMNS);
+  if (warp == WARPS + 1) tmem_alloc(smem_address(&tmem_base_sh), Shape::COLUMNS);
   if (tid == 0) {
     for (int i = 0; i < KS; ++i) {
-      mbar_init(k_full(i), 1);
+      mbar_init(k_full(i), 2);
       mbar_init(k_free(i), 1);
     }
     for (int i = 0; i < QS; ++i) {
@@ -128,8 +169,9 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) weigh_kernel(const __grid_co
     for (int t = 0; t < 2; ++t)
       for (int i = 0; i < 2; ++i) {
         mbar_init(s_full(t, i), 1);
-        mbar_init(s_free(t, i), 4);
+        mbar_init(s_free(t, i), WARPS / 2);
       }
+    for (int i = 0; i < 32; ++i) mbar_init(half_done(0, i), 1);
     stop_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -138,12 +180,12 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) weigh_kernel(const __grid_co
   int64_t* before = (int64_t*)(smem_raw + (k_ring - smem_address(smem_raw)));
   const int S = a.b.streams;
   {
-    const int per = (S + CHUNK_THREADS - 1) / CHUNK_THREADS;
+    const int per = (S + THREADS - 1) / THREADS;
     auto work = [&](int s, bool report) -> int64_t {
       const int n = a.b.count(s), len = a.c.length(s, report);
       return n == 0 ? 0 : (int64_t)((len + WEIGH_KEYS - 1) / WEIGH_KEYS) * ((n + a.tokens - 1) / a.tokens);
     };
-    for (int s = tid; s < S; s += CHUNK_THREADS) before[s] = work(s, blockIdx.x == 0);
+    for (int s = tid; s < S; s += THREADS) before[s] = work(s, blockIdx.x == 0);
     __syncthreads();
     int64_t sum = 0;
     for (int i = 0; i < per; ++i)
@@ -202,7 +244,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) weigh_kernel(const __grid_co
     start_u_sh = u;
   }
   // columns that no copy fills must not hold stale values that are not finite
-  for (int i = tid; i < QS * Shape::Q_TILE / 16; i += CHUNK_THREADS)
+  for (int i = tid; i < QS * Shape::Q_TILE / 16; i += THREADS)
     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(q_ring + 16 * i), "r"(0) : "memory");
   fence_async_smem();
   tmem_fence_before();
@@ -212,70 +254,91 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) weigh_kernel(const __grid_co
   const WeighPlace start = start_sh;
   const int64_t u0 = start_u_sh;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 8) {
-      // ---- copies ----
-      int ks = 0, qs = 0;
-      uint32_t k_phase = 0, q_phase = 0;
-      const int in_page = (1 << a.c.page_shift) - 1;
-      const int boxes = TILE_KEYS / a.box_keys;
-      const uint32_t box_bytes = a.box_keys * 128;
-      for_items(a, start, u0, u1, [&](const WeighPlace& p, int k0, int k1, int2 tok, int steps) {
-        if (steps == 0) return true;
-        for (int key0 = k0; key0 < k1; key0 += TILE_KEYS) {
-          const int box = lane / HALVES, half = lane % HALVES, key = key0 + box * a.box_keys;
-          int page = -1;
-          if (box < boxes && key < k1) {
-            page = a.c.page(p.s, key >> a.c.page_shift);
-            if (page < 0) a.c.flag();
-          }
-          const uint32_t live = __ballot_sync(~0u, page >= 0);
-          if (!mbar_wait(k_free(ks), k_phase ^ 1, stop, status)) return false;
-          if (lane == 0) mbar_expect(k_full(ks), __popc(live) * box_bytes);
-          __syncwarp();
-          if (page >= 0)
-            tma_load_4d(k_ring + ks * Shape::K_TILE + half * K_HALF + box * box_bytes, &a.k_map, 64 * half, key & in_page,
-                        p.h, page, k_full(ks));
-          if (++ks == KS) ks = 0, k_phase ^= 1;
-        }
-        const int row = a.b.begin(p.s) + tok.x;
-        for (int i = 0; i < steps; ++i) {
-          if (!mbar_wait(q_free(qs), q_phase ^ 1, stop, status)) return false;
-          if (lane == 0) {
+  if (warp >= WARPS) {
+    if (warp == WARPS) {
+      // ---- query copies ----
+      int qs = 0;
+      uint32_t q_phase = 0;
+      WeighWalk walk{a, start, u0, u1};
+      bool ok = true;
+      for (WeighItem x = walk.next(); x.there && ok; x = walk.next()) {
+        const int row = a.b.begin(x.s) + x.tok.x;
+        for (int i = 0; i < x.steps && ok; ++i) {
+          if (!(ok = mbar_wait(q_free(qs), q_phase ^ 1, stop, status))) break;
+          if (elect_lane()) {
             mbar_expect(q_full(qs), HALVES * a.tokens * a.group * 128);
             for (int c = 0; c < HALVES; ++c)
-              tma_load_3d(q_ring + qs * Shape::Q_TILE + c * Q_HALF, &a.q_map, 64 * c, p.h * a.group, row + i * a.tokens,
+              tma_load_3d(q_ring + qs * Shape::Q_TILE + c * Q_HALF, &a.q_map, 64 * c, x.h * a.group, row + i * a.tokens,
                           q_full(qs));
           }
           __syncwarp();
           if (++qs == QS) qs = 0, q_phase ^= 1;
         }
-        return true;
-      });
-    } else if (warp == 9) {
+      }
+    } else if (warp >= WARPS + 2) {
+      // ---- key copies, every other one of a tile's ----
+      int ks = 0;
+      uint32_t k_phase = 0;
+      const int in_page = (1 << a.c.page_shift) - 1;
+      const int boxes = TILE_KEYS / a.box_keys;
+      const uint32_t box_bytes = a.box_keys * 128;
+      const int copy = 2 * lane + warp - (WARPS + 2), box = copy / HALVES, half = copy % HALVES;
+      auto page_of = [&](const WeighItem& x, int tile) {   // of this lane's copy
+        const int key = x.k0 + tile * TILE_KEYS + box * a.box_keys;
+        if (!x.there || x.steps == 0 || box >= boxes || key >= x.k1) return -1;
+        const int page = a.c.page(x.s, key >> a.c.page_shift);
+        if (page < 0) a.c.flag();
+        return page;
+      };
+      // page ids are read an item early: their latency hides behind the copies of the item before
+      WeighWalk walk{a, start, u0, u1};
+      WeighItem x = walk.next();
+      int pages[2] = {page_of(x, 0), page_of(x, 1)};
+      bool ok = true;
+      while (x.there && ok) {
+        const WeighItem after = walk.next();
+        const int after_pages[2] = {page_of(after, 0), page_of(after, 1)};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (x.steps == 0 || x.k0 + t * TILE_KEYS >= x.k1) break;
+          const uint32_t live = __ballot_sync(~0u, pages[t] >= 0);
+          if (!(ok = mbar_wait(k_free(ks), k_phase ^ 1, stop, status))) break;
+          if (lane == 0) mbar_expect(k_full(ks), __popc(live) * box_bytes);
+          __syncwarp();
+          if (pages[t] >= 0)
+            tma_load_4d(k_ring + ks * Shape::K_TILE + half * K_HALF + box * box_bytes, &a.k_map, 64 * half,
+                        (x.k0 + t * TILE_KEYS + box * a.box_keys) & in_page, x.h, pages[t], k_full(ks));
+          if (++ks == KS) ks = 0, k_phase ^= 1;
+        }
+        x = after;
+        pages[0] = after_pages[0];
+        pages[1] = after_pages[1];
+      }
+    } else {
       // ---- products ----
       int ks = 0, qs = 0;
       uint32_t k_phase = 0, q_phase = 0, uses[2] = {0, 0};
       constexpr uint32_t KIND = mma_kind<T>(TILE_KEYS, N, false);
-      for_items(a, start, u0, u1, [&](const WeighPlace& p, int k0, int k1, int2, int steps) {
-        if (steps == 0) return true;
-        const int tiles = k1 - k0 > TILE_KEYS ? 2 : 1;
+      WeighWalk walk{a, start, u0, u1};
+      bool ok = true;
+      for (WeighItem x = walk.next(); x.there && ok; x = walk.next()) {
+        if (x.steps == 0) continue;
+        const int tiles = x.k1 - x.k0 > TILE_KEYS ? 2 : 1;
         int k_stage[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (t >= tiles) break;
-          if (!mbar_wait(k_full(ks), k_phase, stop, status)) return false;
+          if (t >= tiles || !ok) break;
+          ok = mbar_wait(k_full(ks), k_phase, stop, status);
           k_stage[t] = ks;
           if (++ks == KS) ks = 0, k_phase ^= 1;
         }
-        for (int i = 0; i < steps; ++i) {
-          if (!mbar_wait(q_full(qs), q_phase, stop, status)) return false;
+        for (int i = 0; i < x.steps && ok; ++i) {
+          if (!(ok = mbar_wait(q_full(qs), q_phase, stop, status))) break;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t >= tiles) break;
             const int buf = uses[t] & 1;
-            if (!mbar_wait(s_free(t, buf), ((uses[t] >> 1) & 1) ^ 1, stop, status)) return false;
+            if (!(ok = mbar_wait(s_free(t, buf), ((uses[t] >> 1) & 1) ^ 1, stop, status))) break;
             ++uses[t];
             tmem_fence_after();
             if (elect_lane()) {
@@ -294,92 +357,164 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) weigh_kernel(const __grid_co
         if (elect_lane())
           for (int t = 0; t < tiles; ++t) mma_commit(k_free(k_stage[t]));
         __syncwarp();
-        return true;
-      });
+      }
     }
   } else {
     // ---- weights ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int tile = warp >> 2;
+    constexpr int MINE = Shape::MY_COLUMNS;
+    const int tile = (warp >> 2) & 1, part = warp >> 3, col0 = part * MINE;   // this warp's columns
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
     const float sc = a.scale * LOG2E;
     const uint64_t sc2 = pack2(sc, sc);
     float* ml = minus_lse[warp];
-    uint32_t uses = 0;
-    for_items(a, start, u0, u1, [&](const WeighPlace& p, int k0, int k1, int2 tok, int steps) {
-      const int key0 = k0 + tile * TILE_KEYS, key = key0 + (tid & 127);
-      if (key0 >= k1) return true;
-      const bool live = key < k1;
-      const int page = live ? a.c.page(p.s, key >> a.c.page_shift) : -1;
-      if (live && page < 0) a.c.flag();
-      const int64_t at = (((int64_t)page * a.n_kv + p.h) << a.c.page_shift) + (key & ((1 << a.c.page_shift) - 1));
-      const float old = page >= 0 ? a.c.mass[at] : 0.f;
-      const int2 mine = live ? tokens_that_see(a, p.n, p.len, key, key + 1) : make_int2(0, 0);
-      const int64_t row0 = a.b.begin(p.s);
-      uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
-      for (int i = 0; i < steps; ++i) {
-        const int t0 = tok.x + i * a.tokens, full = a.tokens * a.group, cols = min(full, (tok.y - t0) * a.group);
-        // this warp's copy of -lse (base 2) of the step's rows; its latency hides behind the wait
-        float nl[(N + 31) / 32];
-        bool odd = false;   // a row whose lse is not finite
+    constexpr int LN = (MINE + 31) / 32;
+    const int full = a.tokens * a.group;
+    int lse_at[LN];   // of this lane's columns, relative to the step's first row
 #pragma unroll
-        for (int e = 0; e < (N + 31) / 32; ++e) {
-          const int c = lane + 32 * e, tk = c / a.group;
-          nl[e] = c < cols ? -LOG2E * a.lse[(row0 + t0 + tk) * a.n_q + p.h * a.group + c - tk * a.group] : -INFINITY;
-          odd |= c < cols && !(fabsf(nl[e]) < INFINITY);
+    for (int e = 0; e < LN; ++e) {
+      const int c = col0 + lane + 32 * e, tk = c / a.group;
+      lse_at[e] = tk * a.n_q + c - tk * a.group;
+    }
+    // Everything that comes from memory is asked for ahead: an item's page two items early, its mass one item, a
+    // step's lse one step; the lengths when a stream is entered.
+    auto my_key = [&](const WeighItem& x) { return x.k0 + tile * TILE_KEYS + (tid & 127); };
+    auto page_of = [&](const WeighItem& x) {
+      const int key = my_key(x);
+      if (!x.there || key >= x.k1) return -1;
+      const int page = a.c.page(x.s, key >> a.c.page_shift);
+      if (page < 0) a.c.flag();
+      return page;
+    };
+    auto mass_at = [&](const WeighItem& x, int page) {
+      return (((int64_t)page * a.n_kv + x.h) << a.c.page_shift) + (my_key(x) & ((1 << a.c.page_shift) - 1));
+    };
+    auto load_lse = [&](const WeighItem& x, int i, float* nl) {
+      const int t0 = x.tok.x + i * a.tokens, cols = min(full, (x.tok.y - t0) * a.group);
+      const float* from = a.lse + ((int64_t)a.b.begin(x.s) + t0) * a.n_q + x.h * a.group;
+#pragma unroll
+      for (int e = 0; e < LN; ++e) nl[e] = col0 + lane + 32 * e < cols ? from[lse_at[e]] : INFINITY;
+    };
+    uint32_t uses = 0, items = 0;
+    WeighWalk walk{a, start, u0, u1};
+    WeighItem x = walk.next(), x1;
+    x1.there = false;
+    if (x.there) x1 = walk.next();
+    int page = page_of(x), page1 = page_of(x1);
+    float old = page >= 0 ? a.c.mass[mass_at(x, page)] : 0.f;
+    float nl[LN];
+    if (x.there && x.steps > 0) load_lse(x, 0, nl);
+    bool ok = true;
+    while (x.there && ok) {
+      WeighItem x2;
+      x2.there = false;
+      if (x1.there) x2 = walk.next();
+      const int page2 = page_of(x2);
+      const float old1 = page1 >= 0 ? a.c.mass[mass_at(x1, page1)] : 0.f;
+      const bool work = x.k0 + tile * TILE_KEYS < x.k1;
+      const int key = my_key(x);
+      const int2 mine = key < x.k1 ? tokens_that_see(a, x.n, x.len, key, key + 1) : make_int2(0, 0);
+      uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
+      for (int i = 0; i < x.steps && work; ++i) {
+        const int t0 = x.tok.x + i * a.tokens, cols = min(full, (x.tok.y - t0) * a.group);
+        bool odd = false;   // a row whose lse is not finite
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < LN; ++e) {
+          const int c = lane + 32 * e;
+          odd |= col0 + c < cols && !(fabsf(nl[e]) < INFINITY);
+          if (c < MINE) ml[c] = -LOG2E * nl[e];
         }
         __syncwarp();
-#pragma unroll
-        for (int e = 0; e < (N + 31) / 32; ++e)
-          if (lane + 32 * e < N) ml[lane + 32 * e] = nl[e];
-        __syncwarp();
+        if (i + 1 < x.steps) load_lse(x, i + 1, nl);
         const int buf = uses & 1;
-        if (!mbar_wait(s_full(tile, buf), (uses >> 1) & 1, stop, status)) return false;
+        if (!(ok = mbar_wait(s_full(tile, buf), (uses >> 1) & 1, stop, status))) break;
         ++uses;
         tmem_fence_after();
-        const uint32_t s_tmem = lanes + (2 * tile + buf) * N;
-        uint32_t x[N];
-#pragma unroll
-        for (int c = 0; c < N; c += 32) {
-          if constexpr (N >= 32) tmem_load32(x + c, s_tmem + c);
-          else tmem_load16(x, s_tmem);
-        }
-        tmem_wait_load();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free(tile, buf));
+        const uint32_t s_tmem = lanes + (2 * tile + buf) * N + col0;
         // columns of the tokens that see this key
         const int lo = (max(mine.x, t0) - t0) * a.group, hi = min((mine.y - t0) * a.group, cols);
         const bool plain = __all_sync(~0u, lo == 0 && hi >= full && !odd);
-        if (plain) {
+        auto release = [&] {
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free(tile, buf));
+        };
+        auto add_plain = [&](const uint32_t* s, int c0, auto width) {
 #pragma unroll
-          for (int c = 0; c < N; c += 4) {   // of every 4 exponentials 2 on the FMA pipe
-            const float4 z = *(const float4*)(ml + c);
-            const float2 y0 = unpack2(fma2(pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, pack2(z.x, z.y)));
-            const uint64_t y1 = fma2(pack2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sc2, pack2(z.z, z.w));
-            sum0 = add2(sum0, pack2(exp2_approx(y0.x), exp2_approx(y0.y)));
-            sum1 = add2(sum1, exp2_fit(y1));
+          for (int c = 0; c < decltype(width)::value; c += 4) {
+            const float4 z = *(const float4*)(ml + c0 + c);
+            const uint64_t y0 = fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, pack2(z.x, z.y));
+            const uint64_t y1 = fma2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc2, pack2(z.z, z.w));
+            sum0 = add2(sum0, exp2_pair(y0));
+            sum1 = add2(sum1, WEIGH_FIT >> (c / 4 & 7) & 1 ? exp2_fit(y1) : exp2_pair(y1));
           }
+        };
+        auto add_some = [&](const uint32_t* s, int c0, auto width) {
+          const int l0 = min(max(lo - col0 - c0, 0), 32), h0 = min(max(hi - col0 - c0, 0), 32);
+          const uint32_t bits = (uint32_t)((1ull << h0) - 1) & ~(uint32_t)((1ull << l0) - 1);
+#pragma unroll
+          for (int c = 0; c < decltype(width)::value; c += 2) {
+            const float2 z = *(const float2*)(ml + c0 + c);
+            const float e0 = exp2_approx(fmaf(__uint_as_float(s[c]), sc, z.x));
+            const float e1 = exp2_approx(fmaf(__uint_as_float(s[c + 1]), sc, z.y));
+            sum0 = add2(sum0, pack2(bits >> c & 1 ? e0 : 0.f, bits >> (c + 1) & 1 ? e1 : 0.f));
+          }
+        };
+        if constexpr (N == 16) {
+          uint32_t s0[16];
+          tmem_load16(s0, s_tmem);
+          tmem_wait_load();
+          release();
+          if (plain) add_plain(s0, 0, std::integral_constant<int, 16>());
+          else add_some(s0, 0, std::integral_constant<int, 16>());
         } else {
-#pragma unroll
-          for (int c = 0; c < N; c += 2) {
-            const float2 z = *(const float2*)(ml + c);
-            const float e0 = exp2_approx(fmaf(__uint_as_float(x[c]), sc, z.x));
-            const float e1 = exp2_approx(fmaf(__uint_as_float(x[c + 1]), sc, z.y));
-            sum0 = add2(sum0, pack2(c >= lo && c < hi ? e0 : 0.f, c + 1 >= lo && c + 1 < hi ? e1 : 0.f));
-          }
+          static_assert(MINE == 64, "two pieces of 32 columns");
+          auto in_turn = [&](auto&& f) {   // 32 columns at a time, the next 32 on their way
+            uint32_t s0[32], s1[32];
+            tmem_load32(s0, s_tmem);
+            tmem_wait_load();
+            tmem_load32(s1, s_tmem + 32);
+            f(s0, 0);
+            tmem_wait_load();
+            release();
+            f(s1, 32);
+          };
+          if (plain) in_turn([&](const uint32_t* s, int c) { add_plain(s, c, std::integral_constant<int, 32>()); });
+          else in_turn([&](const uint32_t* s, int c) { add_some(s, c, std::integral_constant<int, 32>()); });
         }
       }
+      if (!ok) break;
       const float2 both = unpack2(add2(sum0, sum1));
-      if (page >= 0) a.out[at] = a.decay * old + (both.x + both.y);
-      return true;
-    });
+      float sum = both.x + both.y;
+      if constexpr (Shape::HALVES == 2) {
+        // Four buffers and barriers each: the second half is at most three items ahead (score buffers are freed by both).
+        if (work && x.steps > 0) {
+          float* other = &half_sum[items & 3][tid & 255];
+          if (part == 1) {
+            *other = sum;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(half_done(warp & 7, items & 3));
+          } else {
+            if (!(ok = mbar_wait(half_done(warp, items & 3), (items >> 2) & 1, stop, status))) break;
+            sum += *(volatile float*)other;
+          }
+          ++items;
+        }
+      }
+      if (part == 0 && page >= 0) a.out[mass_at(x, page)] = a.decay * old + sum;
+      x = x1;
+      x1 = x2;
+      page = page1;
+      page1 = page2;
+      old = old1;
+      if (x.there && x.steps > 0) load_lse(x, 0, nl);
+    }
   }
   if (*stop)
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   tmem_fence_before();
   __syncthreads();
-  if (warp == 9) tmem_free(tmem, Shape::COLUMNS);
+  if (warp == WARPS + 1) tmem_free(tmem, Shape::COLUMNS);
 }
 
 }  // namespace cache
