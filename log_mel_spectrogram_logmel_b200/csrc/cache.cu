@@ -234,6 +234,8 @@ template <typename T, int D>
 cudaError_t allow_shared_memory() {
   constexpr cudaFuncAttribute LIMIT = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<T, D>, LIMIT, RowsShape<D>::SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(select_kernel<false>, LIMIT, 4 * SELECT_CACHED);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(select_kernel<true>, LIMIT, 4 * SELECT_CACHED);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(attend_chunk_kernel<T, D>, LIMIT, ChunkShape<D>::SMEM);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(weigh_kernel<T, D, 16>, LIMIT, WeighShape<D, 16>::SMEM);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(weigh_kernel<T, D, 128>, LIMIT, WeighShape<D, 128>::SMEM);
@@ -548,8 +550,22 @@ logmel_status logmel_cache_evict(logmel_cache_plan* p, const logmel_cache_view* 
     a.recent = (int)recent;
     a.kept = kept + s0 * c.n_kv_heads * budget;
     const cudaStream_t str = (cudaStream_t)stream;
-    select_kernel<<<dim3(c.n_kv_heads, n), SELECT_THREADS, 0, str>>>(a);
-    if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
+    // a run of about 4,096 slots per CTA at the longest a table row can name
+    int cluster = 1;
+    while (cluster < SELECT_MAX_CLUSTER && (int64_t)cluster * 4096 < a.c.capacity) cluster <<= 1;
+    const int64_t run = std::min<int64_t>(SELECT_CACHED, (a.c.capacity + cluster - 1) / cluster);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t launch{};
+    launch.gridDim = dim3(c.n_kv_heads * cluster, n);
+    launch.blockDim = dim3(SELECT_THREADS);
+    launch.dynamicSmemBytes = 4 * (size_t)run;
+    launch.stream = str;
+    launch.attrs = &attr;
+    launch.numAttrs = 1;
+    CK(cudaLaunchKernelEx(&launch, cluster > 1 ? select_kernel<true> : select_kernel<false>, a));
     gather_kernel<<<dim3((unsigned)((budget + GATHER_ROWS - 1) / GATHER_ROWS), c.n_kv_heads, n), GATHER_THREADS, 0, str>>>(a);
     if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
   }

@@ -1,6 +1,8 @@
 // Token cache: the kernels that move rows (append, evict).  All of them are
 // bound by memory traffic; none computes more than a few operations a byte.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "cache_common.cuh"
 
 namespace logmel {
@@ -132,8 +134,6 @@ struct EvictArgs {
   int* kept;   // [streams, n_kv, budget]
 };
 
-constexpr int SELECT_THREADS = 512;
-
 // Weights as unsigned keys of the same order: -0 as +0, NaN above all.
 __device__ __forceinline__ uint32_t rank_key(float w) {
   if (w != w) return 0xffffffffu;
@@ -151,96 +151,180 @@ __device__ __forceinline__ float slot_mass(const EvictArgs& a, int s, int h, int
   return a.c.mass[((int64_t)p * a.n_kv + h) * size + (j & (size - 1))];
 }
 
-// One CTA per stream and key head: the value of the k-th largest weight by a
-// radix selection (8 bits a pass), then one pass in slot order that writes
-// the kept slots.
+// A cluster of CTAs per stream and key head, each with a run of the slots: the
+// value of the k-th largest weight by radix selection (11, 11 and 10 bits,
+// histograms added up over distributed shared memory), then the kept slots in slot
+// order, behind the counts of the runs before.  The weights are read once and
+// stay in shared memory where a run fits.  The first 11 bits hold the exponent and two
+// bits more, so that weights spread over the counters; zeros, which are many, are
+// counted by vote.  (One CTA per key head that read the weights in every pass took 280 us for streams of 65,536 slots.)
+constexpr int SELECT_MAX_CLUSTER = 8;
+constexpr int SELECT_CACHED = 16384;   // slots of a run kept in shared memory
+
+constexpr int SELECT_THREADS = 512;
+
+struct SelectShared {
+  int hist[2048];
+  int total[2048];
+  int above[32], equal[32];
+  int run[2];          // of this CTA: keys above the threshold, keys equal to it
+  uint32_t prefix;
+  int need;
+};
+
+template <bool CLUSTER>
 __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int warp_sum[2][SELECT_THREADS / 32];
-  __shared__ uint32_t sh_prefix;
-  __shared__ int sh_need;
-  const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int len = a.c.length(s, tid == 0);
+  extern __shared__ uint32_t cached[];
+  __shared__ SelectShared sh;
+  namespace cg = cooperative_groups;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int C = CLUSTER ? cluster.num_blocks() : 1, rank = CLUSTER ? cluster.block_rank() : 0;
+  auto sync_all = [&] {
+    if constexpr (CLUSTER) cluster.sync();
+    else __syncthreads();
+  };
+  const int h = blockIdx.x / C, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int THREADS = SELECT_THREADS, WARPS = THREADS / 32;
+  const int len = a.c.length(s, tid == 0 && rank == 0);
   const int m = min(len, a.budget);
-  const int old = len - min(len, a.recent);     // slots that compete
-  int need = len <= a.budget ? old : m - (len - old);
+  const int newest = min(len, a.recent), old = len - newest;     // the other slots compete
+  int need = m - newest;                                         // and so many of them stay
   int* kept = a.kept + ((int64_t)s * a.n_kv + h) * a.budget;
-  bool bad = false;
-  uint32_t prefix = 0;
-  if (need < old && need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += SELECT_THREADS) hist[i] = 0;
-      __syncthreads();
-      for (int j = tid; j < old; j += SELECT_THREADS) {
-        const uint32_t key = rank_key(slot_mass(a, s, h, j, bad));
-        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int d = 255, left = need;
-        while (d > 0 && hist[d] < left) left -= hist[d--];
-        sh_prefix = prefix | ((uint32_t)d << shift);
-        sh_need = left;
-      }
-      __syncthreads();
-      prefix = sh_prefix;
-      need = sh_need;
-    }
-  }
-  // keys above `prefix` are kept, and of the equal ones the first `need`
-  const bool all = need >= old && len <= a.budget;
-  const bool none = !all && m - (len - old) == 0;
-  int above_before = 0, equal_before = 0;
-  for (int base = 0; base < old; base += SELECT_THREADS) {
-    const int j = base + tid;
-    bool gt = false, eq = false;
-    if (j < old && !none) {
-      if (all) gt = true;
-      else {
-        const uint32_t key = rank_key(slot_mass(a, s, h, j, bad));
-        gt = key > prefix;
-        eq = key == prefix;
-      }
-    }
-    const uint32_t bg = __ballot_sync(~0u, gt), be = __ballot_sync(~0u, eq);
-    if (lane == 0) {
-      warp_sum[0][warp] = __popc(bg);
-      warp_sum[1][warp] = __popc(be);
-    }
-    __syncthreads();
-    int g0 = above_before, e0 = equal_before, gt_all = 0, eq_all = 0;
-    for (int w = 0; w < SELECT_THREADS / 32; ++w) {
-      if (w < warp) {
-        g0 += warp_sum[0][w];
-        e0 += warp_sum[1][w];
-      }
-      gt_all += warp_sum[0][w];
-      eq_all += warp_sum[1][w];
-    }
-    const uint32_t below = (1u << lane) - 1;
-    g0 += __popc(bg & below);
-    e0 += __popc(be & below);
-    if (gt || (eq && e0 < need)) kept[g0 + min(e0, need)] = j;
-    above_before += gt_all;
-    equal_before += eq_all;
-    __syncthreads();
-  }
-  for (int i = tid; i < a.budget; i += SELECT_THREADS) {
+  for (int i = rank * THREADS + tid; i < a.budget; i += C * THREADS) {
     if (i >= m) kept[i] = -1;
-    else if (i >= m - (len - old)) kept[i] = len - (m - i);
+    else if (i >= need) kept[i] = len - (m - i);
+    else if (len == m) kept[i] = i;
+  }
+  if (len == m || need == 0) return;   // the whole cluster
+  bool bad = false;
+  const int per = (old + C - 1) / C, from = min(old, rank * per), to = min(old, from + per);
+  const bool in_smem = per <= SELECT_CACHED;
+  auto key_of = [&](int j) { return in_smem ? cached[j - from] : rank_key(slot_mass(a, s, h, j, bad)); };
+  if (in_smem) {
+#pragma unroll 8
+    for (int j = from + tid; j < to; j += THREADS) cached[j - from] = rank_key(slot_mass(a, s, h, j, bad));
+  }
+  uint32_t prefix = 0;
+  constexpr uint32_t ZERO = 0x80000000u;   // rank_key(0)
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? 2048 : 1024;
+    for (int i = tid; i < bins; i += THREADS) sh.hist[i] = 0;
+    __syncthreads();
+    for (int j0 = from; j0 < to; j0 += THREADS) {
+      const int j = j0 + tid;
+      const uint32_t key = j < to ? key_of(j) : 0u;
+      const bool in = j < to && (pass == 0 || (pass == 1 ? key >> 21 == prefix >> 21 : key >> 10 == prefix >> 10));
+      const uint32_t zeros = __ballot_sync(~0u, in && key == ZERO);
+      const int digit = key >> shift & (bins - 1);
+      if (in && (key != ZERO || lane == __ffs(zeros) - 1)) atomicAdd(&sh.hist[digit], key == ZERO ? __popc(zeros) : 1);
+    }
+    // Every CTA adds up its share of the bins over all histograms and hands the sums to the first, which finds the
+    // digit.
+    __syncthreads();
+    int* total = sh.hist;
+    if constexpr (CLUSTER) {
+      total = sh.total;
+      cluster.sync();
+      const int share = bins / C;
+      for (int i = rank * share + tid; i < (rank + 1) * share; i += THREADS) {
+        int sum = 0;
+#pragma unroll 8
+        for (int r = 0; r < C; ++r) sum += *cluster.map_shared_rank(&sh.hist[i], r);
+        *cluster.map_shared_rank(&sh.total[i], 0) = sum;
+      }
+      cluster.sync();
+    }
+    if (rank == 0) {
+      // where the count from above reaches `need`: a few bins per thread, the largest first
+      const int per_thread = bins / THREADS;
+      int mine = 0;
+      for (int e = 0; e < per_thread; ++e) mine += total[bins - 1 - per_thread * tid - e];
+      int upto = mine;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(~0u, upto, d);
+        if (lane >= d) upto += y;
+      }
+      if (lane == 31) sh.above[warp] = upto;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) upto += sh.above[w];
+      int left = need - (upto - mine);
+      if (left > 0 && left <= mine) {   // one thread
+        int d = bins - 1 - per_thread * tid;
+        while (total[d] < left) left -= total[d--];
+        sh.prefix = prefix | ((uint32_t)d << shift);
+        sh.need = left;
+      }
+      __syncthreads();
+    }
+    if constexpr (CLUSTER) {
+      cluster.sync();
+      prefix = *cluster.map_shared_rank(&sh.prefix, 0);
+      need = *cluster.map_shared_rank(&sh.need, 0);
+    } else {
+      prefix = sh.prefix;
+      need = sh.need;
+    }
+  }
+  // keys above `prefix` stay, and of the equal ones the first `need`: a run of slots per warp
+  const int each = ((to - from + WARPS - 1) / WARPS + 31) & ~31;
+  const int w0 = min(to, from + warp * each), w1 = min(to, w0 + each);
+  int above = 0, equal = 0;
+  for (int j0 = w0; j0 < w1; j0 += 32) {
+    const int j = j0 + lane;
+    const uint32_t key = j < w1 ? key_of(j) : 0u;
+    above += __popc(__ballot_sync(~0u, j < w1 && key > prefix));
+    equal += __popc(__ballot_sync(~0u, j < w1 && key == prefix));
+  }
+  if (lane == 0) {
+    sh.above[warp] = above;
+    sh.equal[warp] = equal;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int g = 0, e = 0;
+    for (int w = 0; w < WARPS; ++w) {
+      g += sh.above[w];
+      e += sh.equal[w];
+    }
+    sh.run[0] = g;
+    sh.run[1] = e;
+  }
+  sync_all();
+  int g = 0, e = 0;
+  if constexpr (CLUSTER)
+    for (int r = 0; r < rank; ++r) {
+      const int* run = cluster.map_shared_rank(sh.run, r);
+      g += run[0];
+      e += run[1];
+    }
+  for (int w = 0; w < warp; ++w) {
+    g += sh.above[w];
+    e += sh.equal[w];
+  }
+  for (int j0 = w0; j0 < w1; j0 += 32) {
+    const int j = j0 + lane;
+    const uint32_t key = j < w1 ? key_of(j) : 0u;
+    const bool gt = j < w1 && key > prefix, eq = j < w1 && key == prefix;
+    const uint32_t bg = __ballot_sync(~0u, gt), be = __ballot_sync(~0u, eq), below = (1u << lane) - 1;
+    const int gi = g + __popc(bg & below), ei = e + __popc(be & below);
+    if (gt || (eq && ei < need)) kept[gi + min(ei, need)] = j;
+    g += __popc(bg);
+    e += __popc(be);
   }
   if (bad) a.c.flag();
+  if constexpr (CLUSTER) cluster.sync();   // no CTA leaves while another reads its shared memory
 }
 
 constexpr int GATHER_ROWS = 32;
 constexpr int GATHER_THREADS = 256;
 
 // Copies the kept rows: one CTA per stream, key head and 32 kept rows; 16
-// bytes per thread and step.
+// bytes per thread and step.  (Done by the selecting CTAs, which are few, the copy was slower than both kernels.)
 __global__ void __launch_bounds__(GATHER_THREADS) gather_kernel(const __grid_constant__ EvictArgs a) {
   const int s = blockIdx.z, h = blockIdx.y, r0 = blockIdx.x * GATHER_ROWS;
   const int len = a.c.length(s, false);
-  const int m = min(min(len, a.budget), a.to.capacity);
+  const int m = min(len, a.budget);   // budget is within what a table row of `to` can name
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.to.lens[s] = m;
   if (r0 >= m) return;
   const int per_row = a.head_dim >> 3, rows = min(GATHER_ROWS, m - r0), size = 1 << a.c.page_shift;

@@ -189,6 +189,18 @@ def test_attend(lm, name, new, lens, layout, dtype):
         assert b.plan.device_status() == 0
 
 
+@pytest.mark.parametrize("new,lens", [([400], [9000]), ([130, 9, 260], [5000, 3000, 2600]), ([700] * 4, [900, 800, 3000, 700]),
+                                      ([1500], [1500]), ([300] * 30, [300 + 10 * i for i in range(30)])])
+def test_attend_long(lm, new, lens):
+    """Many tiles of keys for a CTA: the ring goes round, items are split and joined, whole items go first."""
+    for layout, dtype in (((16, 8, 128), torch.bfloat16), ((4, 4, 64), torch.float16)):
+        b = Box(lm, *layout, 64, dtype, new, lens, seed=1)
+        b.check_attend()
+        b.check_attend(window=700)
+        b.check_weigh()
+        assert b.plan.device_status() == 0
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("causal,window", [(True, 1), (True, 50), (True, 128), (False, 0), (False, 70), (True, 10**12)])
 def test_attend_masks_and_pages(lm, page, causal, window):
@@ -489,6 +501,14 @@ def test_evict_orders_special_weights(lm):
     _evict_case(lm, [40, 333], 35, 0, mass=lambda b: b.mass.fill_(1e-42))
     _evict_case(lm, [2000], 777, 10, ties=False)
     _evict_case(lm, [9000, 4000], 2048, 100, layout=(2, 2, 128), page=128, seed=4)
+
+
+@pytest.mark.parametrize("lens,page", [([5000, 7], 16), ([8000, 4096], 64), ([16000], 16), ([33000, 20000], 256)])
+def test_evict_long_streams(lm, lens, page):
+    """Streams that several CTAs select from together, ties in plenty among them."""
+    for ties in (True, False):
+        _evict_case(lm, lens, 1500, 200, layout=(2, 1, 64), page=page, ties=ties, seed=page)
+    _evict_case(lm, lens, 1500, 0, layout=(2, 1, 64), page=page, mass=lambda b: b.mass.zero_())
 
 
 def test_evict_within_one_pool(lm):
