@@ -145,6 +145,10 @@ def _offsets(offsets) -> np.ndarray:
     return off
 
 
+def _address(a: np.ndarray) -> int:
+    return a.__array_interface__["data"][0]
+
+
 def _ptr64(a: np.ndarray):
     return a.ctypes.data_as(_i64p)
 
@@ -500,6 +504,11 @@ class CachePlan:
                    "logmel_cache_plan_create")
         self._h = h
         self._destroy = _lib.logmel_cache_plan_destroy   # kept: module globals may be gone at exit
+        # looked up once: a call on one new token costs the host more than the GPU
+        self._index = self.device.index
+        self._layout = (self.device, self.dtype, n_kv_heads, head_dim, page_size)
+        self._tensor, self._empty, self._int32, self._float32 = torch.Tensor, torch.empty, torch.int32, torch.float32
+        self._current_stream = torch._C._cuda_getCurrentRawStream
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -515,6 +524,9 @@ class CachePlan:
         _check(_lib.logmel_cache_rotary(ctypes.addressof(self._config), inv.ctypes.data, ctypes.addressof(length)),
                "logmel_cache_rotary")
         return inv[:self.rotary_dim // 2], length.value
+
+    def _stream(self, stream):
+        return self._current_stream(self._index) if stream is None else stream.cuda_stream
 
     def device_status(self, stream=None) -> int:
         """Reads and clears the status word (logmel_cache_device_status): 4 when a
@@ -572,6 +584,7 @@ class TokenCache:
                                 mass.data_ptr() if mass is not None else None, shape[0], self.n_streams,
                                 table.shape[1], strides(k_pages), strides(v_pages))
         self._view_ptr = ctypes.addressof(self._view)
+        self._uniform = {}   # offsets of pushes of the same number of tokens for every stream, by that number
 
     @classmethod
     def empty(cls, plan: CachePlan, n_streams: int, max_tokens: int) -> "TokenCache":
@@ -587,36 +600,42 @@ class TokenCache:
                    torch.zeros(shape[:3], dtype=torch.float32, device=plan.device))
 
     def _offsets(self, offsets, rows):
+        """Host address of the offsets, and the array that holds them."""
         if offsets is None:
-            if rows % max(self.n_streams, 1):
+            n, rest = divmod(rows, self.n_streams) if self.n_streams else (0, rows)
+            if rest:
                 raise ValueError(f"{rows} rows are not the same number for each of {self.n_streams} streams")
-            n = rows // max(self.n_streams, 1)
-            return np.arange(self.n_streams + 1, dtype=np.int64) * n
+            off = self._uniform.get(n)
+            if off is None:
+                off = np.arange(self.n_streams + 1, dtype=np.int64) * n
+                if len(self._uniform) < 64:
+                    self._uniform[n] = off
+            return _address(off), off
         off = _offsets(offsets)
         if off.shape[0] != self.n_streams + 1:
             raise ValueError("offsets must hold n_streams + 1 entries")
         if off[0] != 0 or off[-1] != rows:
             raise ValueError(f"offsets must run from 0 to the {rows} rows given")
-        return off
+        return _address(off), off
 
     def _rows(self, t, heads, name, rows=None):
         plan = self.plan
-        if not isinstance(t, _torch().Tensor) or not t.is_cuda or t.dtype != plan.dtype:
+        if not isinstance(t, plan._tensor) or t.dtype is not plan.dtype or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA {plan.dtype} tensor")
-        if t.device != plan.device:
+        if t.get_device() != plan._index:
             raise ValueError(f"{name} is on {t.device}, the plan on {plan.device}")
         shape = t.shape
-        if len(shape) != 3 or shape[1] != heads or shape[2] != plan.head_dim or rows not in (None, shape[0]):
+        if len(shape) != 3 or shape[1] != heads or shape[2] != plan.head_dim or (rows is not None and rows != shape[0]):
             raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {heads}, {plan.head_dim}]")
-        st = t.stride()
-        if st[2] != 1:
+        row, head, last = t.stride()
+        if last != 1:
             raise ValueError(f"the head dimension of {name} must be contiguous")
         # strides of dimensions of size one are never used
-        return _Rows(t.data_ptr(), st[0] if shape[0] > 1 else heads * plan.head_dim, st[1] if heads > 1 else plan.head_dim)
+        return _Rows(t.data_ptr(), row if shape[0] > 1 else heads * plan.head_dim, head if heads > 1 else plan.head_dim)
 
-    def _new(self, like, heads, stream):
-        torch = _torch()
-        out = torch.empty((like.shape[0], heads, self.plan.head_dim), dtype=self.plan.dtype, device=self.plan.device)
+    def _new(self, rows, heads, stream):
+        plan = self.plan
+        out = plan._empty((rows, heads, plan.head_dim), dtype=plan.dtype, device=plan.device)
         if stream is not None:
             out.record_stream(stream)
         return out
@@ -629,24 +648,24 @@ class TokenCache:
         rows into streams, default the same number each; positions (CUDA
         int32 [rows]) default to the rows' slots.  Returns the turned queries
         (q_out, which may be q)."""
-        torch, plan = _torch(), self.plan
+        plan = self.plan
         rq = self._rows(q, plan.n_q_heads, "q")
         rows = q.shape[0]
         rk, rv = self._rows(k, plan.n_kv_heads, "k", rows), self._rows(v, plan.n_kv_heads, "v", rows)
-        off = self._offsets(offsets, rows)
+        off, _held = self._offsets(offsets, rows)
         pos = None
         if positions is not None:
-            if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or positions.device != plan.device:
+            if not isinstance(positions, plan._tensor) or positions.dtype != plan._int32 or positions.device != plan.device:
                 raise TypeError("positions must be an int32 tensor on the plan's device")
             if positions.shape != (rows,) or not positions.is_contiguous():
                 raise ValueError("positions must hold one contiguous entry per row")
             pos = positions.data_ptr()
         if q_out is None:
-            q_out = self._new(q, plan.n_q_heads, stream)
+            q_out = self._new(rows, plan.n_q_heads, stream)
         ro = self._rows(q_out, plan.n_q_heads, "q_out", rows)
-        _check(_lib.logmel_cache_append(plan._h, self._view_ptr, off.ctypes.data, ctypes.addressof(rq),
+        _check(_lib.logmel_cache_append(plan._h, self._view_ptr, off, ctypes.addressof(rq),
                                         ctypes.addressof(rk), ctypes.addressof(rv), pos, ctypes.addressof(ro),
-                                        _stream_handle(stream, plan.device)), "logmel_cache_append")
+                                        plan._stream(stream)), "logmel_cache_append")
         return q_out
 
     def attend(self, q, offsets=None, causal: bool = True, window: int = 0, out=None, return_lse: bool = False,
@@ -655,21 +674,21 @@ class TokenCache:
         [rows, n_q_heads, head_dim], and with return_lse also the logarithm of each
         row's sum, float32 [rows, n_q_heads].  window > 0 limits every row to
         the newest `window` slots up to its own."""
-        torch, plan = _torch(), self.plan
+        plan = self.plan
         rq = self._rows(q, plan.n_q_heads, "q")
         rows = q.shape[0]
-        off = self._offsets(offsets, rows)
+        off, _held = self._offsets(offsets, rows)
         if out is None:
-            out = self._new(q, plan.n_q_heads, stream)
+            out = self._new(rows, plan.n_q_heads, stream)
         ro = self._rows(out, plan.n_q_heads, "out", rows)
         lse = None
         if return_lse:
-            lse = torch.empty((rows, plan.n_q_heads), dtype=torch.float32, device=plan.device)
+            lse = plan._empty((rows, plan.n_q_heads), dtype=plan._float32, device=plan.device)
             if stream is not None:
                 lse.record_stream(stream)
-        _check(_lib.logmel_cache_attend(plan._h, self._view_ptr, off.ctypes.data, ctypes.addressof(rq),
+        _check(_lib.logmel_cache_attend(plan._h, self._view_ptr, off, ctypes.addressof(rq),
                                         ctypes.addressof(ro), lse.data_ptr() if return_lse else None,
-                                        int(bool(causal)), int(window), _stream_handle(stream, plan.device)),
+                                        int(bool(causal)), int(window), plan._stream(stream)),
                "logmel_cache_attend")
         return (out, lse) if return_lse else out
 
@@ -678,12 +697,12 @@ class TokenCache:
         """Adds the attention weight that the cached keys received from the
         new rows (logmel_cache_weigh): out = decay * mass + the weights, for every live
         slot of the streams with new rows.  out defaults to mass itself."""
-        torch, plan = _torch(), self.plan
+        plan = self.plan
         if self.mass is None:
             raise ValueError("the cache has no mass tensor")
         rq = self._rows(q, plan.n_q_heads, "q")
         rows = q.shape[0]
-        off = self._offsets(offsets, rows)
+        off, _held = self._offsets(offsets, rows)
         _check_cuda_f32(lse, "lse", plan.device)
         if lse.shape != (rows, plan.n_q_heads):
             raise ValueError(f"lse must be [{rows}, {plan.n_q_heads}]")
@@ -693,9 +712,9 @@ class TokenCache:
             _check_cuda_f32(out, "out", plan.device)
             if out.shape != self.mass.shape:
                 raise ValueError("out must have the shape of mass")
-        _check(_lib.logmel_cache_weigh(plan._h, self._view_ptr, off.ctypes.data, ctypes.addressof(rq), lse.data_ptr(),
+        _check(_lib.logmel_cache_weigh(plan._h, self._view_ptr, off, ctypes.addressof(rq), lse.data_ptr(),
                                        int(bool(causal)), int(window), float(decay), out.data_ptr(),
-                                       _stream_handle(stream, plan.device)), "logmel_cache_weigh")
+                                       plan._stream(stream)), "logmel_cache_weigh")
         return out
 
     def evict(self, to: "TokenCache", budget: int, recent: int = 0, stream=None):
@@ -703,15 +722,15 @@ class TokenCache:
         `recent` and of the others the heaviest, and writes them in order
         into `to` (logmel_cache_evict), whose lens and mass are set too.  Returns their
         old slots, int32 [n_streams, n_kv_heads, budget], padded with -1."""
-        torch, plan = _torch(), self.plan
+        plan = self.plan
         if not isinstance(to, TokenCache):
             raise TypeError("to must be a TokenCache")
         a, b = plan, to.plan
-        if (b.device, b.dtype, b.n_kv_heads, b.head_dim, b.page_size) != (a.device, a.dtype, a.n_kv_heads, a.head_dim, a.page_size):
+        if a is not b and a._layout != b._layout:
             raise ValueError("to must have the layout of this cache")
-        kept = torch.empty((self.n_streams, plan.n_kv_heads, max(int(budget), 0)), dtype=torch.int32, device=plan.device)
+        kept = plan._empty((self.n_streams, plan.n_kv_heads, max(int(budget), 0)), dtype=plan._int32, device=plan.device)
         if stream is not None:
             kept.record_stream(stream)
         _check(_lib.logmel_cache_evict(plan._h, self._view_ptr, to._view_ptr, int(budget), int(recent),
-                                       kept.data_ptr(), _stream_handle(stream, plan.device)), "logmel_cache_evict")
+                                       kept.data_ptr(), plan._stream(stream)), "logmel_cache_evict")
         return kept

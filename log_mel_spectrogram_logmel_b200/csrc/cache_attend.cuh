@@ -25,7 +25,7 @@ struct AttendArgs {
 // few rows
 // ---------------------------------------------------------------------------
 // The rows of one (stream, key head) fill one 16-row tensor-core tile; its
-// keys are cut into units of 16.  All units of the launch form one line,
+// keys are cut into units of 8 KB (16 keys of 128 dimensions, 32 of 64).  All units of the launch form one line,
 // (stream, key head, unit), which is cut into equal runs, one per warp: every
 // warp gets the same number of bytes whatever the lengths are, and no host
 // knowledge of the lengths is needed.  A warp copies its units through a ring
@@ -40,8 +40,10 @@ constexpr int ROWS_MIN_UNITS = 4;             // a shorter run costs more in joi
 
 template <int D>
 struct RowsShape {
-  static constexpr int STAGES = D == 128 ? 3 : 6;
-  static constexpr int HALF = ROWS_TILE * D * 2;          // bytes of 16 keys
+  static constexpr int STAGES = 3;
+  static constexpr int KEYS = D == 128 ? 16 : 32;         // of a unit
+  static constexpr int SHIFT = D == 128 ? 4 : 5;
+  static constexpr int HALF = KEYS * D * 2;               // bytes of a unit's keys
   static constexpr int STAGE = 2 * HALF;                  // keys, then values
   static constexpr int SMEM = ROWS_WARPS * STAGES * STAGE;
   static constexpr int PART = ROWS_TILE * (D + 2);        // floats of a split tile: m, l, rows
@@ -104,7 +106,7 @@ struct Place {
 template <typename T, int D>
 __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel(const __grid_constant__ AttendArgs a) {
   using Shape = RowsShape<D>;
-  constexpr int STAGES = Shape::STAGES, CHUNKS = D / 8, KSTEPS = D / 16, NT = D / 8;
+  constexpr int STAGES = Shape::STAGES, CHUNKS = D / 8, KSTEPS = D / 16, NT = D / 8, KEYS = Shape::KEYS, GROUPS = KEYS / 16;
   extern __shared__ __align__(128) char smem[];
   __shared__ int64_t before[ROWS_WARPS * 32 + 1];   // units (of one key head) before each thread's streams
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
     int64_t sum = 0;
     for (int i = 0; i < per_thread; ++i) {
       const int s = tid * per_thread + i;
-      if (s < a.b.streams) sum += extent_of(a, s, 4, blockIdx.x == 0).units;
+      if (s < a.b.streams) sum += extent_of(a, s, Shape::SHIFT, blockIdx.x == 0).units;
     }
     int64_t run = sum;
     for (int d = 1; d < 32; d <<= 1) {
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
     int64_t u = before[lo] * a.n_kv;
     at.s = lo * per_thread;
     for (;; ++at.s) {
-      at.e = extent_of(a, at.s, 4, false);
+      at.e = extent_of(a, at.s, Shape::SHIFT, false);
       const int64_t here = (int64_t)at.e.units * a.n_kv;
       if (u0 < u + here) break;
       u += here;
@@ -164,49 +166,74 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
     p.unit = 0;
     if (++p.h < a.n_kv) return;
     p.h = 0;
-    do p.e = extent_of(a, ++p.s, 4, false);
+    do p.e = extent_of(a, ++p.s, Shape::SHIFT, false);
     while (p.e.units == 0);
   };
-  auto page_of = [&](const Place& p) {
-    const int key = (p.e.first + p.unit) << 4;
-    if (key >= p.e.hi) return -2;   // the one unit of rows that see nothing
-    return a.c.page(p.s, key >> a.c.page_shift);
+  // page ids of a unit, one per 16 keys; -2: no key there is seen
+  struct Pages {
+    int id[GROUPS];
+  };
+  auto pages_of = [&](const Place& p) {
+    Pages g;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+      const int key = ((p.e.first + p.unit) << Shape::SHIFT) + 16 * i;
+      g.id[i] = key >= p.e.hi ? -2 : a.c.page(p.s, key >> a.c.page_shift);
+    }
+    return g;
   };
 
   // ring
   const uint32_t ring = smem_address(smem) + warp * STAGES * Shape::STAGE;
-  constexpr int ROWS_PER_STEP = 32 / CHUNKS, STEPS = ROWS_TILE / ROWS_PER_STEP;
+  constexpr int ROWS_PER_STEP = 32 / CHUNKS, STEPS = 16 / ROWS_PER_STEP;   // of 16 keys
   const int my_row = lane / CHUNKS, my_chunk = lane % CHUNKS;
   const int in_page = (1 << a.c.page_shift) - 1;
-  auto issue = [&](const Place& p, int page, int stage) {
-    const int key = (p.e.first + p.unit) << 4;
-    if (page == -1 && lane == 0) a.c.flag();
-    const char* k = a.c.k;
-    const char* v = a.c.v;
-    const int at0 = key & in_page;
-    if (page >= 0) {
-      k += 2 * ((int64_t)page * a.c.k_page + p.h * a.c.k_head + (at0 + my_row) * a.c.k_slot + 8 * my_chunk);
-      v += 2 * ((int64_t)page * a.c.v_page + p.h * a.c.v_head + (at0 + my_row) * a.c.v_slot + 8 * my_chunk);
-    }
-    const uint32_t dst = ring + stage * Shape::STAGE;
+  const int64_t k_step = (int64_t)ROWS_PER_STEP * 2 * a.c.k_slot, v_step = (int64_t)ROWS_PER_STEP * 2 * a.c.v_slot;
+  auto issue = [&](const Place& p, const Pages& pages, int stage) {
+    const int key0 = (p.e.first + p.unit) << Shape::SHIFT;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int r = my_row + i * ROWS_PER_STEP;
-      const bool live = page >= 0 && key + r >= p.e.lo && key + r < p.e.hi;
-      const uint32_t off = r * (D * 2) + ((my_chunk ^ (r & 7)) << 4);
-      copy16(dst + off, live ? k + (int64_t)i * ROWS_PER_STEP * 2 * a.c.k_slot : a.c.k, live);
-      copy16(dst + Shape::HALF + off, live ? v + (int64_t)i * ROWS_PER_STEP * 2 * a.c.v_slot : a.c.v, live);
+    for (int g = 0; g < GROUPS; ++g) {
+      const int key = key0 + 16 * g, page = pages.id[g];
+      if (page == -1 && lane == 0) a.c.flag();
+      const char* k = a.c.k;
+      const char* v = a.c.v;
+      if (page >= 0) {
+        const int at0 = (key & in_page) + my_row;
+        k += 2 * ((int64_t)page * a.c.k_page + p.h * a.c.k_head + at0 * a.c.k_slot + 8 * my_chunk);
+        v += 2 * ((int64_t)page * a.c.v_page + p.h * a.c.v_head + at0 * a.c.v_slot + 8 * my_chunk);
+      }
+      const uint32_t dst = ring + stage * Shape::STAGE + g * 16 * D * 2;
+      if (page >= 0 && key >= p.e.lo && key + 16 <= p.e.hi) {   // every key is seen
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const int r = my_row + i * ROWS_PER_STEP;
+          const uint32_t off = r * (D * 2) + ((my_chunk ^ (r & 7)) << 4);
+          copy16(dst + off, k, true);
+          copy16(dst + Shape::HALF + off, v, true);
+          k += k_step;
+          v += v_step;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const int r = my_row + i * ROWS_PER_STEP;
+          const bool live = page >= 0 && key + r >= p.e.lo && key + r < p.e.hi;
+          const uint32_t off = r * (D * 2) + ((my_chunk ^ (r & 7)) << 4);
+          copy16(dst + off, live ? k + i * k_step : a.c.k, live);
+          copy16(dst + Shape::HALF + off, live ? v + i * v_step : a.c.v, live);
+        }
+      }
     }
   };
   Place ahead = at;
   int64_t ahead_u = u0;
-  int ahead_page = page_of(ahead);
+  Pages ahead_pages = pages_of(ahead);
   auto produce = [&](int stage) {
     if (ahead_u < u1) {
-      issue(ahead, ahead_page, stage);
+      issue(ahead, ahead_pages, stage);
       if (++ahead_u < u1) {
         step(ahead);
-        ahead_page = page_of(ahead);   // read one unit early: its latency hides behind this unit
+        ahead_pages = pages_of(ahead);   // read one unit early: the latency hides behind this unit
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -258,22 +285,32 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
     __syncwarp();
     produce(stage == 0 ? STAGES - 1 : stage - 1);   // the stage that the previous unit left
     const uint32_t ks = ring + stage * Shape::STAGE, vs = ks + Shape::HALF;
-    const int key = (at.e.first + at.unit) << 4;
+    const int key = (at.e.first + at.unit) << Shape::SHIFT;
 
-    // scores of 16 rows x 16 keys
-    float x[2][4] = {};
+    // scores of 16 rows x KEYS keys, in two sums each: half the chain of dependent products
+    float x[2 * GROUPS][4], y[2 * GROUPS][4];
 #pragma unroll
-    for (int j = 0; j < KSTEPS; ++j) {
-      uint32_t b[4];
-      const int r = (lane & 7) + ((lane & 16) >> 1), c = 2 * j + ((lane >> 3) & 1);
-      ldmatrix4(b, ks + r * (D * 2) + ((c ^ (r & 7)) << 4));
-      mma16816<T>(x[0], q[j], b[0], b[1]);
-      mma16816<T>(x[1], q[j], b[2], b[3]);
-    }
-    const bool edge = key < all_see.x || key + 16 > all_see.y;
+    for (int t = 0; t < 2 * GROUPS; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[t][e] = y[t][e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < KSTEPS; ++j)
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        uint32_t b[4];
+        const int r = (lane & 7) + ((lane & 16) >> 1), c = 2 * j + ((lane >> 3) & 1);
+        ldmatrix4(b, ks + g * 16 * D * 2 + r * (D * 2) + ((c ^ (r & 7)) << 4));
+        mma16816<T>(j & 1 ? y[2 * g] : x[2 * g], q[j], b[0], b[1]);
+        mma16816<T>(j & 1 ? y[2 * g + 1] : x[2 * g + 1], q[j], b[2], b[3]);
+      }
+#pragma unroll
+    for (int t = 0; t < 2 * GROUPS; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[t][e] += y[t][e];
+    const bool edge = key < all_see.x || key + KEYS > all_see.y;
     if (edge) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2 * GROUPS; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = key + 8 * t + 2 * gc + (e & 1), i = e >> 1;
@@ -284,7 +321,9 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
     bool grew = false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float t = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
+      float t = fmaxf(x[0][2 * i], x[0][2 * i + 1]);
+#pragma unroll
+      for (int e = 1; e < 2 * GROUPS; ++e) t = fmaxf(t, fmaxf(x[e][2 * i], x[e][2 * i + 1]));
       t = fmaxf(t, __shfl_xor_sync(~0u, t, 1));
       t = fmaxf(t, __shfl_xor_sync(~0u, t, 2));
       top[i] = fmaxf(m[i], t * sc);
@@ -305,62 +344,64 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) use[i] = m[i] == -INFINITY ? 0.f : m[i];
-    uint32_t p[4];
+    uint32_t p[GROUPS][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2 * GROUPS; ++t)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float p0 = exp2_approx(fmaf(x[t][2 * i], sc, -use[i])), p1 = exp2_approx(fmaf(x[t][2 * i + 1], sc, -use[i]));
         l[i] += p0 + p1;                                        // summed before the weights are rounded
-        p[2 * t + i] = Half2<T>::from_float(p0, p1);
+        p[t >> 1][2 * (t & 1) + i] = Half2<T>::from_float(p0, p1);
       }
     // Values that are not finite may only reach the rows that see them, and
     // 0 x inf is not 0: where rows differ in what they see, look first.
     bool apart = false;
     if (edge && mixed_rows) {
-      bool bad = false;
-      for (int i = lane; i < ROWS_TILE * CHUNKS; i += 32) {
+      uint32_t acc = 0;
+      for (int i = lane; i < KEYS * CHUNKS; i += 32) {
         uint32_t w[4];
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(vs + 16 * i));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          constexpr uint32_t E = Half2<T>::EXPONENT;
-          bad |= (w[e] & E & 0xffffu) == (E & 0xffffu) || (w[e] & E & 0xffff0000u) == (E & 0xffff0000u);
-        }
+        for (int e = 0; e < 4; ++e) acc = Half2<T>::times_zero(w[e], acc);
       }
-      apart = __any_sync(~0u, bad);
+      apart = __any_sync(~0u, (acc & 0x7fff7fffu) != 0);
     }
     const int vr = (lane & 7) + (lane & 8), vc = lane >> 4;
     if (!apart) {
 #pragma unroll
-      for (int j = 0; j < NT / 2; ++j) {
-        uint32_t b[4];
-        ldmatrix4_trans(b, vs + vr * (D * 2) + (((2 * j + vc) ^ (vr & 7)) << 4));
-        mma16816<T>(o[2 * j], p, b[0], b[1]);
-        mma16816<T>(o[2 * j + 1], p, b[2], b[3]);
-      }
-    } else {
-      for (int e = 0; e < 16; ++e) {   // one key at a time, added only to the rows that see it
-        const uint32_t mine = (e >> 1 & 3) == gc ? (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
-        const uint32_t lo = e < 8 ? mine : 0u, hi = e < 8 ? 0u : mine;
-        const uint32_t pe[4] = {p[0] & lo, p[1] & lo, p[2] & hi, p[3] & hi};
-        bool sees[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) sees[i] = key + e >= row_seen[i].x && key + e < row_seen[i].y;
+      for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
         for (int j = 0; j < NT / 2; ++j) {
           uint32_t b[4];
-          ldmatrix4_trans(b, vs + vr * (D * 2) + (((2 * j + vc) ^ (vr & 7)) << 4));
+          ldmatrix4_trans(b, vs + g * 16 * D * 2 + vr * (D * 2) + (((2 * j + vc) ^ (vr & 7)) << 4));
+          mma16816<T>(o[2 * j], p[g], b[0], b[1]);
+          mma16816<T>(o[2 * j + 1], p[g], b[2], b[3]);
+        }
+    } else {
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            float y[4] = {};
-            mma16816<T>(y, pe, b[2 * t] & lo, b[2 * t + 1] & hi);
+      for (int g = 0; g < GROUPS; ++g)
+#pragma unroll 1
+        for (int e = 0; e < 16; ++e) {   // one key at a time, added only to the rows that see it
+          const uint32_t mine = (e >> 1 & 3) == gc ? (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
+          const uint32_t lo = e < 8 ? mine : 0u, hi = e < 8 ? 0u : mine;
+          const uint32_t pe[4] = {p[g][0] & lo, p[g][1] & lo, p[g][2] & hi, p[g][3] & hi};
+          bool sees[2];
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-              if (sees[w >> 1]) o[2 * j + t][w] += y[w];
+          for (int i = 0; i < 2; ++i) sees[i] = key + 16 * g + e >= row_seen[i].x && key + 16 * g + e < row_seen[i].y;
+#pragma unroll
+          for (int j = 0; j < NT / 2; ++j) {
+            uint32_t b[4];
+            ldmatrix4_trans(b, vs + g * 16 * D * 2 + vr * (D * 2) + (((2 * j + vc) ^ (vr & 7)) << 4));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              float z[4] = {};
+              mma16816<T>(z, pe, b[2 * t] & lo, b[2 * t + 1] & hi);
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                if (sees[w >> 1]) o[2 * j + t][w] += z[w];
+            }
           }
         }
-      }
     }
     if (++stage == STAGES) stage = 0;
 
@@ -415,24 +456,40 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
         __threadfence();
         auto slot = [&](int w) { return a.parts + (int64_t)(2 * w + (w == first ? 1 : 0)) * Shape::PART; };
         for (int r = 0; r < rows; ++r) {
+          // the lanes share the parts' maxima and sums, then the row's columns; 8 parts' columns are under way at a time
           float mm = -INFINITY;
           for (int w = first + lane; w <= last; w += 32) mm = fmaxf(mm, __ldcg(slot(w) + r));
           for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
           const float base = mm == -INFINITY ? 0.f : mm;
           constexpr int V = D / 32;
           float acc[V] = {}, sum = 0.f;
-#pragma unroll 8
-          for (int w = first; w <= last; ++w) {
-            const float* s = slot(w);
-            const float f = exp2_approx(__ldcg(s + r) - base);
-            sum += f * __ldcg(s + ROWS_TILE + r);
+          for (int w0 = first; w0 <= last; w0 += 32) {
+            float f = 0.f;
+            if (w0 + lane <= last) {
+              f = exp2_approx(__ldcg(slot(w0 + lane) + r) - base);
+              sum += f * __ldcg(slot(w0 + lane) + ROWS_TILE + r);
+            }
+            const int n = min(32, last - w0 + 1);
+            for (int i = 0; i < n; i += 8) {
+              float2 z[8][V / 2];
 #pragma unroll
-            for (int e = 0; e < V; e += 2) {
-              const float2 y = __ldcg((const float2*)(s + 2 * ROWS_TILE + r * D + V * lane + e));
-              acc[e] += f * y.x;
-              acc[e + 1] += f * y.y;
+              for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k)
+                  if (i + e < n) z[e][k] = __ldcg((const float2*)(slot(w0 + i + e) + 2 * ROWS_TILE + r * D + V * lane) + k);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float fe = __shfl_sync(~0u, f, i + e);
+                if (i + e < n)
+#pragma unroll
+                  for (int k = 0; k < V / 2; ++k) {
+                    acc[2 * k] += fe * z[e][k].x;
+                    acc[2 * k + 1] += fe * z[e][k].y;
+                  }
+              }
             }
           }
+          for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
           const int tok = r / a.group, hq = at.h * a.group + r - tok * a.group;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           T* out = (T*)a.out.data + (t0 + tok) * a.out.row + (int64_t)hq * a.out.head;
