@@ -502,6 +502,8 @@ logmel_status logmel_cache_weigh(logmel_cache_plan* p, const logmel_cache_view* 
   a.window = (int)std::min<int64_t>(window, INT32_MAX / 2 + 1);
   a.scale = p->scale;
   a.decay = decay;
+  a.tickets = p->d_tickets;
+  a.parts = p->d_parts;
   a.out = mass_out;
   Launches it{offsets, cache->n_streams};
   int64_t s0, r0;

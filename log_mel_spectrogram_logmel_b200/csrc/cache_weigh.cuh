@@ -7,15 +7,15 @@
 // A weight needs no running maximum: exp(x - lse) with the row's known lse.
 //
 // An item is 256 slots of one (stream, key head), two 128-key tiles.  Its
-// query rows come in steps of N columns that both tiles share.  Items are
-// dealt to the CTAs in runs of equal numbers of steps.  N = 16 serves pushes of
-// few rows, where reading the keys is the bound and the ring holds 6 tiles of
-// them; N = 128 the others, bound by the exponentials (one per pair of row
-// and key against 2 x head_dim tensor-core operations).
+// query rows come in steps of N columns that both tiles share.  All steps of the launch
+// form one line that is cut into equal runs, one per CTA.  The sums of an
+// item that falls into several runs are added in the order of the runs by the
+// warp that finishes last.  N = 16 serves pushes of few rows, where reading the keys is the
+// bound and the ring holds 6 tiles of them; N = 128 the others, bound by the exponentials (one per
+// pair of row and key against 2 x head_dim tensor-core operations) and what surrounds them.
 //
-// Roles: the weight warps (8, or with N = 128 16 of which two share a key and
-// take half of the columns each: two warps a scheduler wait too long on their own
-// results), then one warp that copies queries, one that issues the MMAs into
+// Roles: the weight warps, which own 32 keys each (with N = 128 two warps share
+// them and take half of the columns each), then one warp that copies queries, one that issues the MMAs into
 // two score buffers per tile, and two that copy keys, half of a tile's copies each (with
 // pages of 16 slots a tile is 16 copies, more than one warp issues in time).
 #pragma once
@@ -35,6 +35,8 @@ struct WeighArgs {
   int n_q, n_kv, group;
   int causal, window;
   float scale, decay;
+  int* tickets;        // eight per CTA, zero between calls
+  float* parts;        // sums of split items, two per CTA
   CUtensorMap q_map, k_map;
   int tokens;          // tokens of a step: N / group
   int box_keys;        // slots a key copy brings
@@ -46,76 +48,68 @@ struct WeighShape {
   static constexpr int K_STAGES = N == 128 ? 3 : 6, Q_STAGES = N == 128 ? 3 : 4;
   static constexpr int SMEM = 1024 + K_STAGES * K_TILE + Q_STAGES * Q_TILE;
   static constexpr int COLUMNS = N == 128 ? 512 : 64;   // tensor memory: two score buffers per tile
-  static constexpr int HALVES = N == 128 ? 2 : 1;       // weight warps per key
-  static constexpr int WARPS = 8 * HALVES, THREADS = 32 * (WARPS + 4);
-  static constexpr int MY_COLUMNS = N / HALVES;
+  static constexpr int PARTS = N == 128 ? 2 : 1;        // weight warps that share a key
+  static constexpr int WARPS = 8 * PARTS, THREADS = 32 * (WARPS + 4);
+  static constexpr int MY_COLUMNS = N / PARTS;
 };
 
 constexpr int WEIGH_KEYS = 2 * TILE_KEYS;
-#ifndef WFIT
-#define WFIT 0x55
-#endif
-constexpr uint32_t WEIGH_FIT = WFIT;
-
+constexpr uint32_t WEIGH_FIT = 0x55;   // of every 8 pairs of exponentials beside 8 on the special-function unit, those
+                                       // computed on the FMA pipe
 // Which tokens of a push see some of the slots [k0, k1): [begin, end).
 __device__ __forceinline__ int2 tokens_that_see(const WeighArgs& a, int n, int len, int k0, int k1) {
   const int p0 = len - n;   // slot of token 0
   const int begin = a.causal ? max(0, k0 - p0) : 0;
-  // token i sees no slot at or below p0 + i - window
-  const int end = a.window > 0 ? (int)max((int64_t)0, min((int64_t)n, (int64_t)k1 - 1 - p0 + a.window)) : n;
+  // token i sees no slot at or below p0 + i - window; a window is at most 2^30 and so are lengths
+  const int end = a.window > 0 ? max(0, min(n, k1 - 1 - p0 + a.window)) : n;
   return make_int2(min(begin, end), end);
 }
 
 struct WeighPlace {
   int s, h, item;
-  int n, len, items;
+  int n, len, items, steps;   // steps of an item on the line
 
   __device__ void load_stream(const WeighArgs& a) {
     n = a.b.count(s);
     len = a.c.length(s, false);
     items = n == 0 ? 0 : (len + WEIGH_KEYS - 1) / WEIGH_KEYS;
+    steps = (n + a.tokens - 1) / a.tokens;
   }
-  __device__ int steps_each(const WeighArgs& a) const { return max(1, (n + a.tokens - 1) / a.tokens); }
-  // to the next item of the line; false at its end
-  __device__ bool next(const WeighArgs& a) {
-    if (++item < items) return true;
+  // to the next item of the line, which exists
+  __device__ void next(const WeighArgs& a) {
+    if (++item < items) return;
     item = 0;
-    if (++h < a.n_kv) return true;
+    if (++h < a.n_kv) return;
     h = 0;
     do {
-      if (++s >= a.b.streams) return false;
+      ++s;
       load_stream(a);
     } while (items == 0);
-    return true;
   }
 };
 
-// An item, the tokens that see some of it, and their steps.
+// What a CTA does of an item: steps [i0, i1) of the tokens that see some of it.
 struct WeighItem {
   int s, h, k0, k1;     // slots [k0, k1)
   int n, len;
   int2 tok;
-  int steps;
-  bool there;
+  int i0, i1;
+  int64_t begin;        // of the item on the line
+  int planned, off;     // steps on the line, and how many of them lie before this run
+  bool whole, there;
 };
 
-// The items of a CTA: those that begin in [u, u1).
+// The items of a CTA's run [u, u1), from place `p` (step `off` of it) on.
 struct WeighWalk {
   const WeighArgs& a;
   WeighPlace p;
+  int off;
   int64_t u, u1;
-  bool first = true;
 
   __device__ WeighItem next() {
     WeighItem x;
-    x.there = false;
-    if (!first) {
-      u += p.steps_each(a);
-      if (u >= u1 || !p.next(a)) u = u1;
-    }
-    first = false;
-    if (u >= u1) return x;
-    x.there = true;
+    x.there = u < u1;
+    if (!x.there) return x;
     x.s = p.s;
     x.h = p.h;
     x.n = p.n;
@@ -123,7 +117,18 @@ struct WeighWalk {
     x.k0 = p.item * WEIGH_KEYS;
     x.k1 = min(p.len, x.k0 + WEIGH_KEYS);
     x.tok = tokens_that_see(a, p.n, p.len, x.k0, x.k1);
-    x.steps = (x.tok.y - x.tok.x + a.tokens - 1) / a.tokens;
+    x.planned = p.steps;
+    const int rows = x.tok.y - x.tok.x;   // all of the push's: as many steps as planned; else not more
+    const int steps = rows == p.n ? p.steps : (rows + a.tokens - 1) / a.tokens;
+    x.off = off;
+    x.begin = u - off;
+    const int upto = (int)min((int64_t)x.planned, off + (u1 - u));
+    x.i0 = min(off, steps);
+    x.i1 = min(upto, steps);
+    x.whole = off == 0 && upto == x.planned;
+    u += upto - off;
+    off = 0;
+    if (u < u1) p.next(a);
     return x;
   }
 };
@@ -139,9 +144,9 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
   __shared__ int stop_sh;
   __shared__ int64_t warp_total[THREADS / 32];
   __shared__ WeighPlace start_sh;
-  __shared__ int64_t start_u_sh;
+  __shared__ int start_off_sh;
   __shared__ alignas(16) float minus_lse[WARPS][Shape::MY_COLUMNS];
-  __shared__ float half_sum[4][Shape::HALVES == 2 ? 256 : 1];   // of an item, from the warps of the second half
+  __shared__ float part_sum[4][Shape::PARTS == 2 ? WEIGH_KEYS : 1];   // of an item, from the warps of the second part
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* stop = &stop_sh;
   int* status = a.c.status;
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
   auto q_free = [&](int i) { return bar0 + 8 * (2 * KS + QS + i); };
   auto s_full = [&](int tile, int buf) { return bar0 + 8 * (2 * KS + 2 * QS + 2 * tile + buf); };
   auto s_free = [&](int tile, int buf) { return bar0 + 8 * (2 * KS + 2 * QS + 4 + 2 * tile + buf); };
-  auto half_done = [&](int w, int buf) { return bar0 + 8 * (2 * KS + 2 * QS + 8 + 4 * w + buf); };   // per warp of the first half
+  auto summed = [&](int w, int buf) { return bar0 + 8 * (2 * KS + 2 * QS + 8 + 4 * w + buf); };   // per warp of the first part
 
   if (warp == WARPS + 1) tmem_alloc(smem_address(&tmem_base_sh), Shape::COLUMNS);
   if (tid == 0) {
@@ -171,7 +176,7 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
         mbar_init(s_full(t, i), 1);
         mbar_init(s_free(t, i), WARPS / 2);
       }
-    for (int i = 0; i < 32; ++i) mbar_init(half_done(0, i), 1);
+    for (int i = 0; i < 32; ++i) mbar_init(summed(0, i), 1);
     stop_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -212,36 +217,24 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
   }
   const int64_t total = before[S] * a.n_kv;
   const int64_t quota = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
-  const int64_t u1 = min(total, (int64_t)(blockIdx.x + 1) * quota);
-  if (tid == 0) {
-    // the first item that begins in [blockIdx.x * quota, u1)
-    const int64_t want = (int64_t)blockIdx.x * quota;
-    int64_t u = u1;
-    if (want < u1) {
-      int lo = 0, hi = S - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (before[mid] * a.n_kv <= want) lo = mid;
-        else hi = mid - 1;
-      }
-      WeighPlace p;
-      p.s = lo;
-      p.load_stream(a);
-      const int64_t per_head = before[lo + 1] - before[lo], steps = p.steps_each(a);
-      int64_t left = want - before[lo] * a.n_kv;
-      p.h = (int)(left / per_head);
-      left -= p.h * per_head;
-      p.item = (int)((left + steps - 1) / steps);
-      u = before[lo] * a.n_kv + p.h * per_head + p.item * steps;
-      bool there = true;
-      if (p.item >= p.items) {
-        p.item = p.items - 1;
-        there = p.next(a);
-      }
-      if (!there) u = u1;
-      start_sh = p;
+  const int64_t u0 = min(total, (int64_t)blockIdx.x * quota), u1 = min(total, u0 + quota);
+  if (tid == 0 && u0 < u1) {
+    int lo = 0, hi = S - 1;   // last stream that begins at or before u0 (so it has steps)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (before[mid] * a.n_kv <= u0) lo = mid;
+      else hi = mid - 1;
     }
-    start_u_sh = u;
+    WeighPlace p;
+    p.s = lo;
+    p.load_stream(a);
+    const int64_t per_head = before[lo + 1] - before[lo];
+    int64_t left = u0 - before[lo] * a.n_kv;
+    p.h = (int)(left / per_head);
+    left -= p.h * per_head;
+    p.item = (int)(left / p.steps);
+    start_off_sh = (int)(left - (int64_t)p.item * p.steps);
+    start_sh = p;
   }
   // columns that no copy fills must not hold stale values that are not finite
   for (int i = tid; i < QS * Shape::Q_TILE / 16; i += THREADS)
@@ -252,18 +245,18 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
   tmem_fence_after();
   const uint32_t tmem = tmem_base_sh;
   const WeighPlace start = start_sh;
-  const int64_t u0 = start_u_sh;
+  const int start_off = start_off_sh;
 
   if (warp >= WARPS) {
     if (warp == WARPS) {
       // ---- query copies ----
       int qs = 0;
       uint32_t q_phase = 0;
-      WeighWalk walk{a, start, u0, u1};
+      WeighWalk walk{a, start, start_off, u0, u1};
       bool ok = true;
       for (WeighItem x = walk.next(); x.there && ok; x = walk.next()) {
         const int row = a.b.begin(x.s) + x.tok.x;
-        for (int i = 0; i < x.steps && ok; ++i) {
+        for (int i = x.i0; i < x.i1 && ok; ++i) {
           if (!(ok = mbar_wait(q_free(qs), q_phase ^ 1, stop, status))) break;
           if (elect_lane()) {
             mbar_expect(q_full(qs), HALVES * a.tokens * a.group * 128);
@@ -285,13 +278,13 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
       const int copy = 2 * lane + warp - (WARPS + 2), box = copy / HALVES, half = copy % HALVES;
       auto page_of = [&](const WeighItem& x, int tile) {   // of this lane's copy
         const int key = x.k0 + tile * TILE_KEYS + box * a.box_keys;
-        if (!x.there || x.steps == 0 || box >= boxes || key >= x.k1) return -1;
+        if (!x.there || x.i0 == x.i1 || box >= boxes || key >= x.k1) return -1;
         const int page = a.c.page(x.s, key >> a.c.page_shift);
         if (page < 0) a.c.flag();
         return page;
       };
       // page ids are read an item early: their latency hides behind the copies of the item before
-      WeighWalk walk{a, start, u0, u1};
+      WeighWalk walk{a, start, start_off, u0, u1};
       WeighItem x = walk.next();
       int pages[2] = {page_of(x, 0), page_of(x, 1)};
       bool ok = true;
@@ -300,7 +293,7 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
         const int after_pages[2] = {page_of(after, 0), page_of(after, 1)};
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (x.steps == 0 || x.k0 + t * TILE_KEYS >= x.k1) break;
+          if (x.i0 == x.i1 || x.k0 + t * TILE_KEYS >= x.k1) break;
           const uint32_t live = __ballot_sync(~0u, pages[t] >= 0);
           if (!(ok = mbar_wait(k_free(ks), k_phase ^ 1, stop, status))) break;
           if (lane == 0) mbar_expect(k_full(ks), __popc(live) * box_bytes);
@@ -319,10 +312,10 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
       int ks = 0, qs = 0;
       uint32_t k_phase = 0, q_phase = 0, uses[2] = {0, 0};
       constexpr uint32_t KIND = mma_kind<T>(TILE_KEYS, N, false);
-      WeighWalk walk{a, start, u0, u1};
+      WeighWalk walk{a, start, start_off, u0, u1};
       bool ok = true;
       for (WeighItem x = walk.next(); x.there && ok; x = walk.next()) {
-        if (x.steps == 0) continue;
+        if (x.i0 == x.i1) continue;
         const int tiles = x.k1 - x.k0 > TILE_KEYS ? 2 : 1;
         int k_stage[2];
 #pragma unroll
@@ -332,7 +325,7 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
           k_stage[t] = ks;
           if (++ks == KS) ks = 0, k_phase ^= 1;
         }
-        for (int i = 0; i < x.steps && ok; ++i) {
+        for (int i = x.i0; i < x.i1 && ok; ++i) {
           if (!(ok = mbar_wait(q_full(qs), q_phase, stop, status))) break;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -361,15 +354,15 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
     }
   } else {
     // ---- weights ----
-    constexpr int MINE = Shape::MY_COLUMNS;
-    const int tile = (warp >> 2) & 1, part = warp >> 3, col0 = part * MINE;   // this warp's columns
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    constexpr int COLS = Shape::MY_COLUMNS, LN = (COLS + 31) / 32;   // 16 or 64 columns
+    const int quarter = warp & 3, tile = (warp >> 2) & 1, part = warp >> 3, col0 = part * COLS;
+    const int my_slot = tile * TILE_KEYS + 32 * quarter + lane;      // of an item's 256
+    const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
     const float sc = a.scale * LOG2E;
     const uint64_t sc2 = pack2(sc, sc);
     float* ml = minus_lse[warp];
-    constexpr int LN = (MINE + 31) / 32;
     const int full = a.tokens * a.group;
-    int lse_at[LN];   // of this lane's columns, relative to the step's first row
+    int lse_at[LN];   // of this lane's columns, relative to a step's first row
 #pragma unroll
     for (int e = 0; e < LN; ++e) {
       const int c = col0 + lane + 32 * e, tk = c / a.group;
@@ -377,62 +370,61 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
     }
     // Everything that comes from memory is asked for ahead: an item's page two items early, its mass one item, a
     // step's lse one step; the lengths when a stream is entered.
-    auto my_key = [&](const WeighItem& x) { return x.k0 + tile * TILE_KEYS + (tid & 127); };
     auto page_of = [&](const WeighItem& x) {
-      const int key = my_key(x);
+      const int key = x.k0 + my_slot;
       if (!x.there || key >= x.k1) return -1;
       const int page = a.c.page(x.s, key >> a.c.page_shift);
       if (page < 0) a.c.flag();
       return page;
     };
     auto mass_at = [&](const WeighItem& x, int page) {
-      return (((int64_t)page * a.n_kv + x.h) << a.c.page_shift) + (my_key(x) & ((1 << a.c.page_shift) - 1));
+      return (((int64_t)page * a.n_kv + x.h) << a.c.page_shift) + ((x.k0 + my_slot) & ((1 << a.c.page_shift) - 1));
     };
     auto load_lse = [&](const WeighItem& x, int i, float* nl) {
       const int t0 = x.tok.x + i * a.tokens, cols = min(full, (x.tok.y - t0) * a.group);
       const float* from = a.lse + ((int64_t)a.b.begin(x.s) + t0) * a.n_q + x.h * a.group;
 #pragma unroll
-      for (int e = 0; e < LN; ++e) nl[e] = col0 + lane + 32 * e < cols ? from[lse_at[e]] : INFINITY;
+      for (int e = 0; e < LN; ++e) nl[e] = lane + 32 * e < COLS && col0 + lane + 32 * e < cols ? from[lse_at[e]] : INFINITY;
     };
     uint32_t uses = 0, items = 0;
-    WeighWalk walk{a, start, u0, u1};
+    WeighWalk walk{a, start, start_off, u0, u1};
     WeighItem x = walk.next(), x1;
     x1.there = false;
     if (x.there) x1 = walk.next();
     int page = page_of(x), page1 = page_of(x1);
-    float old = page >= 0 ? a.c.mass[mass_at(x, page)] : 0.f;
+    float old = page >= 0 && part == 0 ? a.c.mass[mass_at(x, page)] : 0.f;
     float nl[LN];
-    if (x.there && x.steps > 0) load_lse(x, 0, nl);
+    if (x.there && x.i0 < x.i1) load_lse(x, x.i0, nl);
     bool ok = true;
     while (x.there && ok) {
       WeighItem x2;
       x2.there = false;
       if (x1.there) x2 = walk.next();
       const int page2 = page_of(x2);
-      const float old1 = page1 >= 0 ? a.c.mass[mass_at(x1, page1)] : 0.f;
-      const bool work = x.k0 + tile * TILE_KEYS < x.k1;
-      const int key = my_key(x);
-      const int2 mine = key < x.k1 ? tokens_that_see(a, x.n, x.len, key, key + 1) : make_int2(0, 0);
+      const float old1 = page1 >= 0 && part == 0 ? a.c.mass[mass_at(x1, page1)] : 0.f;
+      const bool work = x.i0 < x.i1 && x.k0 + tile * TILE_KEYS < x.k1;
+      const int key = x.k0 + my_slot;
+      const int2 seen_by = key < x.k1 ? tokens_that_see(a, x.n, x.len, key, key + 1) : make_int2(0, 0);
       uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
-      for (int i = 0; i < x.steps && work; ++i) {
+      for (int i = x.i0; i < x.i1 && work; ++i) {
         const int t0 = x.tok.x + i * a.tokens, cols = min(full, (x.tok.y - t0) * a.group);
         bool odd = false;   // a row whose lse is not finite
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < LN; ++e) {
           const int c = lane + 32 * e;
-          odd |= col0 + c < cols && !(fabsf(nl[e]) < INFINITY);
-          if (c < MINE) ml[c] = -LOG2E * nl[e];
+          odd |= c < COLS && col0 + c < cols && !(fabsf(nl[e]) < INFINITY);
+          if (c < COLS) ml[c] = -LOG2E * nl[e];
         }
         __syncwarp();
-        if (i + 1 < x.steps) load_lse(x, i + 1, nl);
+        if (i + 1 < x.i1) load_lse(x, i + 1, nl);
         const int buf = uses & 1;
         if (!(ok = mbar_wait(s_full(tile, buf), (uses >> 1) & 1, stop, status))) break;
         ++uses;
         tmem_fence_after();
         const uint32_t s_tmem = lanes + (2 * tile + buf) * N + col0;
         // columns of the tokens that see this key
-        const int lo = (max(mine.x, t0) - t0) * a.group, hi = min((mine.y - t0) * a.group, cols);
+        const int lo = (max(seen_by.x, t0) - t0) * a.group, hi = min((seen_by.y - t0) * a.group, cols);
         const bool plain = __all_sync(~0u, lo == 0 && hi >= full && !odd);
         auto release = [&] {
           tmem_fence_before();
@@ -460,7 +452,7 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
             sum0 = add2(sum0, pack2(bits >> c & 1 ? e0 : 0.f, bits >> (c + 1) & 1 ? e1 : 0.f));
           }
         };
-        if constexpr (N == 16) {
+        if constexpr (COLS == 16) {
           uint32_t s0[16];
           tmem_load16(s0, s_tmem);
           tmem_wait_load();
@@ -468,8 +460,8 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
           if (plain) add_plain(s0, 0, std::integral_constant<int, 16>());
           else add_some(s0, 0, std::integral_constant<int, 16>());
         } else {
-          static_assert(MINE == 64, "two pieces of 32 columns");
-          auto in_turn = [&](auto&& f) {   // 32 columns at a time, the next 32 on their way
+          static_assert(COLS == 64, "two pieces of 32 columns");
+          auto in_turn = [&](auto&& f) {   // the second 32 columns are on their way while the first are added
             uint32_t s0[32], s1[32];
             tmem_load32(s0, s_tmem);
             tmem_wait_load();
@@ -485,29 +477,49 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
       }
       if (!ok) break;
       const float2 both = unpack2(add2(sum0, sum1));
-      float sum = both.x + both.y;
-      if constexpr (Shape::HALVES == 2) {
-        // Four buffers and barriers each: the second half is at most three items ahead (score buffers are freed by both).
-        if (work && x.steps > 0) {
-          float* other = &half_sum[items & 3][tid & 255];
+      float mine = both.x + both.y;
+      if constexpr (Shape::PARTS == 2) {
+        // Four buffers and barriers each: the second part is at most three items ahead (score buffers are freed by both).
+        if (work) {
+          float* other = &part_sum[items & 3][my_slot];
           if (part == 1) {
-            *other = sum;
+            *other = mine;
             __syncwarp();
-            if (lane == 0) mbar_arrive(half_done(warp & 7, items & 3));
+            if (lane == 0) mbar_arrive(summed(warp & 7, items & 3));
           } else {
-            if (!(ok = mbar_wait(half_done(warp, items & 3), (items >> 2) & 1, stop, status))) break;
-            sum += *(volatile float*)other;
+            if (!(ok = mbar_wait(summed(warp, items & 3), (items >> 2) & 1, stop, status))) break;
+            mine += *(volatile float*)other;
           }
           ++items;
         }
       }
-      if (part == 0 && page >= 0) a.out[mass_at(x, page)] = a.decay * old + sum;
+      if (part == 0) {
+        if (!x.whole) {   // (only with N = 128: with 16 columns an item is one step)
+          const int first = (int)(x.begin / quota), last = (int)((x.begin + x.planned - 1) / quota);
+          auto slot = [&](int w) { return a.parts + (int64_t)(2 * w + (w == first ? 1 : 0)) * WEIGH_KEYS + my_slot; };
+          __stcg(slot(blockIdx.x), mine);
+          __threadfence();
+          __syncwarp();
+          int ticket = 0;
+          if (lane == 0) ticket = atomicAdd(a.tickets + 8 * first + warp, 1);
+          ticket = __shfl_sync(~0u, ticket, 0);
+          if (ticket == last - first) {
+            if (lane == 0) a.tickets[8 * first + warp] = 0;   // ready for the next call
+            __threadfence();
+            mine = 0.f;
+            for (int w = first; w <= last; ++w) mine += __ldcg(slot(w));
+          } else {
+            page = -1;   // another CTA's to write
+          }
+        }
+        if (page >= 0) a.out[mass_at(x, page)] = a.decay * old + mine;
+      }
       x = x1;
       x1 = x2;
       page = page1;
       page1 = page2;
       old = old1;
-      if (x.there && x.steps > 0) load_lse(x, 0, nl);
+      if (x.there && x.i0 < x.i1) load_lse(x, x.i0, nl);
     }
   }
   if (*stop)
