@@ -455,41 +455,8 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
         if (lane == 0) a.tickets[first] = 0;   // ready for the next call
         __threadfence();
         auto slot = [&](int w) { return a.parts + (int64_t)(2 * w + (w == first ? 1 : 0)) * Shape::PART; };
-        for (int r = 0; r < rows; ++r) {
-          // the lanes share the parts' maxima and sums, then the row's columns; 8 parts' columns are under way at a time
-          float mm = -INFINITY;
-          for (int w = first + lane; w <= last; w += 32) mm = fmaxf(mm, __ldcg(slot(w) + r));
-          for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
-          const float base = mm == -INFINITY ? 0.f : mm;
-          constexpr int V = D / 32;
-          float acc[V] = {}, sum = 0.f;
-          for (int w0 = first; w0 <= last; w0 += 32) {
-            float f = 0.f;
-            if (w0 + lane <= last) {
-              f = exp2_approx(__ldcg(slot(w0 + lane) + r) - base);
-              sum += f * __ldcg(slot(w0 + lane) + ROWS_TILE + r);
-            }
-            const int n = min(32, last - w0 + 1);
-            for (int i = 0; i < n; i += 8) {
-              float2 z[8][V / 2];
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-#pragma unroll
-                for (int k = 0; k < V / 2; ++k)
-                  if (i + e < n) z[e][k] = __ldcg((const float2*)(slot(w0 + i + e) + 2 * ROWS_TILE + r * D + V * lane) + k);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float fe = __shfl_sync(~0u, f, i + e);
-                if (i + e < n)
-#pragma unroll
-                  for (int k = 0; k < V / 2; ++k) {
-                    acc[2 * k] += fe * z[e][k].x;
-                    acc[2 * k + 1] += fe * z[e][k].y;
-                  }
-              }
-            }
-          }
-          for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+        constexpr int V = D / 32;   // columns of a lane
+        auto write_row = [&](int r, const float* acc, float sum, float mm) {
           const int tok = r / a.group, hq = at.h * a.group + r - tok * a.group;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           T* out = (T*)a.out.data + (t0 + tok) * a.out.row + (int64_t)hq * a.out.head;
@@ -497,6 +464,88 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
           for (int e = 0; e < V; e += 2)
             *(uint32_t*)(out + V * lane + e) = sum == 0.f ? 0u : Half2<T>::from_float(acc[e] * inv, acc[e + 1] * inv);
           if (a.lse && lane == 0) a.lse[(t0 + tok) * a.n_q + hq] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * LN2;
+        };
+        if (rows > 4) {
+          // Many rows: a lane has a row's maximum and sum, then all rows' columns of a part are under way together.
+          // (Row by row, the 16 rows of a windowed push took a warp 20 us of waiting.)
+          const int r = lane & (ROWS_TILE - 1);
+          float mm = -INFINITY, sum = 0.f;
+          if (r < rows)
+            for (int w = first; w <= last; ++w) mm = fmaxf(mm, __ldcg(slot(w) + r));
+          const float base = mm == -INFINITY ? 0.f : mm;
+          if (r < rows)
+            for (int w = first; w <= last; ++w) sum += exp2_approx(__ldcg(slot(w) + r) - base) * __ldcg(slot(w) + ROWS_TILE + r);
+          constexpr int TOGETHER = D == 128 ? 8 : 16;   // 32 values and 32 sums a lane
+#pragma unroll 1
+          for (int i0 = 0; i0 < rows; i0 += TOGETHER) {
+            float acc[TOGETHER][V];
+#pragma unroll
+            for (int i = 0; i < TOGETHER; ++i)
+#pragma unroll
+              for (int e = 0; e < V; ++e) acc[i][e] = 0.f;
+#pragma unroll 1
+            for (int w = first; w <= last; ++w) {
+              const float f = r < rows ? exp2_approx(__ldcg(slot(w) + r) - base) : 0.f;
+              float2 z[TOGETHER][V / 2];
+#pragma unroll
+              for (int i = 0; i < TOGETHER; ++i)
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k)
+                  z[i][k] = i0 + i < rows ? __ldcg((const float2*)(slot(w) + 2 * ROWS_TILE + (i0 + i) * D + V * lane) + k)
+                                          : make_float2(0.f, 0.f);
+#pragma unroll
+              for (int i = 0; i < TOGETHER; ++i) {
+                const float fi = __shfl_sync(~0u, f, i0 + i);
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) {
+                  acc[i][2 * k] += fi * z[i][k].x;
+                  acc[i][2 * k + 1] += fi * z[i][k].y;
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < TOGETHER; ++i) {
+              const float si = __shfl_sync(~0u, sum, i0 + i), mi = __shfl_sync(~0u, mm, i0 + i);
+              if (i0 + i < rows) write_row(i0 + i, acc[i], si, mi);
+            }
+          }
+        } else {
+          for (int r = 0; r < rows; ++r) {
+            // the lanes share the parts' maxima and sums, then the row's columns; 8 parts' columns are under way at a time
+            float mm = -INFINITY;
+            for (int w = first + lane; w <= last; w += 32) mm = fmaxf(mm, __ldcg(slot(w) + r));
+            for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
+            const float base = mm == -INFINITY ? 0.f : mm;
+            float acc[V] = {}, sum = 0.f;
+            for (int w0 = first; w0 <= last; w0 += 32) {
+              float f = 0.f;
+              if (w0 + lane <= last) {
+                f = exp2_approx(__ldcg(slot(w0 + lane) + r) - base);
+                sum += f * __ldcg(slot(w0 + lane) + ROWS_TILE + r);
+              }
+              const int n = min(32, last - w0 + 1);
+              for (int i = 0; i < n; i += 8) {
+                float2 z[8][V / 2];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+#pragma unroll
+                  for (int k = 0; k < V / 2; ++k)
+                    if (i + e < n) z[e][k] = __ldcg((const float2*)(slot(w0 + i + e) + 2 * ROWS_TILE + r * D + V * lane) + k);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float fe = __shfl_sync(~0u, f, i + e);
+                  if (i + e < n)
+#pragma unroll
+                    for (int k = 0; k < V / 2; ++k) {
+                      acc[2 * k] += fe * z[e][k].x;
+                      acc[2 * k + 1] += fe * z[e][k].y;
+                    }
+                }
+              }
+            }
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+            write_row(r, acc, sum, mm);
+          }
         }
       }
     }

@@ -170,6 +170,9 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
       TMEM_W8(v, 8), "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::TMEM_W8(v, 0), "r"(addr) : "memory");
+}
 
 // --- two fp32 operations in one instruction -------------------------------------
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
