@@ -394,6 +394,8 @@ logmel_status logmel_partition_streams(int64_t n_streams, int n_parts, int64_t* 
  *     and a slot below zero are never followed.  The kernel stores
  *     LOGMEL_DEVICE_BAD_CACHE in the plan's device status word; rows of that
  *     stream then hold no meaningful values, other streams are not affected.
+ *   - Streams may share pages that are only read (attend).  A page that append
+ *     or weigh writes must belong to one stream of the call.
  *   - The plan's scratch is shared by its calls: order calls on one plan on
  *     the GPU (one stream, or events), replayed graphs included.  The calls
  *     allocate nothing and never synchronise, so all of them may be captured.
@@ -503,7 +505,8 @@ logmel_status logmel_cache_weigh(logmel_cache_plan* plan, const logmel_cache_vie
  * [n_streams, n_kv_heads, budget]) receives their old slots, ascending, then -1.
  * `to` has the same n_streams, its own table, and lens other than cache->lens;
  * it may use pages of the same pool that no stream of `cache` has in use (a
- * page both read and written is a race).  Both views need mass.
+ * page both read and written is a race; the same table over the same pages is
+ * refused).  Both views need mass.
  * LOGMEL_ERR_INVALID_ARG unless 1 <= budget <= to's table_width * page_size and
  * 0 <= recent <= budget. */
 logmel_status logmel_cache_evict(logmel_cache_plan* plan, const logmel_cache_view* cache,
@@ -511,7 +514,9 @@ logmel_status logmel_cache_evict(logmel_cache_plan* plan, const logmel_cache_vie
                                  void* stream);
 
 /* Reads and clears the plan's device status word (synchronises `stream`):
- * 0, LOGMEL_DEVICE_BAD_CACHE or LOGMEL_DEVICE_WAIT_TIMEOUT. */
+ * 0, LOGMEL_DEVICE_BAD_CACHE or LOGMEL_DEVICE_WAIT_TIMEOUT (a bounded wait
+ * inside a kernel ran out, about 0.3 s: the results of the calls since the
+ * last read are not complete). */
 logmel_status logmel_cache_device_status(logmel_cache_plan* plan, int* code, void* stream);
 
 /* Test hook for the bounded wait on a tile's span copies (not for normal

@@ -33,8 +33,8 @@ import os
 
 import numpy as np
 
-__all__ = ["Plan", "Stream", "CachePlan", "TokenCache", "LogMelError", "compute_noalloc", "encoder_chunks", "stream_windows", "chunk_views",
-           "partition_utterances", "partition_streams", "lib_path", "exported_symbols", "STATUS"]
+__all__ = ["Plan", "Stream", "CachePlan", "TokenCache", "LogMelError", "compute_noalloc", "encoder_chunks",
+           "stream_windows", "chunk_views", "partition_utterances", "partition_streams", "lib_path", "exported_symbols", "STATUS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "liblogmel_b200.so")
@@ -143,6 +143,11 @@ def _offsets(offsets) -> np.ndarray:
     if off.ndim != 1 or off.shape[0] < 1:
         raise ValueError("offsets must be a 1-D CSR array of n_utt + 1 int64 entries")
     return off
+
+
+def _int64(x) -> int:
+    """Within int64, which ctypes does not check."""
+    return max(-1, min(int(x), 1 << 62))
 
 
 def _address(a: np.ndarray) -> int:
@@ -655,7 +660,8 @@ class TokenCache:
         off, _held = self._offsets(offsets, rows)
         pos = None
         if positions is not None:
-            if not isinstance(positions, plan._tensor) or positions.dtype != plan._int32 or positions.device != plan.device:
+            if (not isinstance(positions, plan._tensor) or positions.dtype != plan._int32
+                    or positions.device != plan.device):
                 raise TypeError("positions must be an int32 tensor on the plan's device")
             if positions.shape != (rows,) or not positions.is_contiguous():
                 raise ValueError("positions must hold one contiguous entry per row")
@@ -688,7 +694,7 @@ class TokenCache:
                 lse.record_stream(stream)
         _check(_lib.logmel_cache_attend(plan._h, self._view_ptr, off, ctypes.addressof(rq),
                                         ctypes.addressof(ro), lse.data_ptr() if return_lse else None,
-                                        int(bool(causal)), int(window), plan._stream(stream)),
+                                        int(bool(causal)), _int64(window), plan._stream(stream)),
                "logmel_cache_attend")
         return (out, lse) if return_lse else out
 
@@ -713,7 +719,7 @@ class TokenCache:
             if out.shape != self.mass.shape:
                 raise ValueError("out must have the shape of mass")
         _check(_lib.logmel_cache_weigh(plan._h, self._view_ptr, off, ctypes.addressof(rq), lse.data_ptr(),
-                                       int(bool(causal)), int(window), float(decay), out.data_ptr(),
+                                       int(bool(causal)), _int64(window), float(decay), out.data_ptr(),
                                        plan._stream(stream)), "logmel_cache_weigh")
         return out
 
@@ -728,9 +734,12 @@ class TokenCache:
         a, b = plan, to.plan
         if a is not b and a._layout != b._layout:
             raise ValueError("to must have the layout of this cache")
-        kept = plan._empty((self.n_streams, plan.n_kv_heads, max(int(budget), 0)), dtype=plan._int32, device=plan.device)
+        if budget > to.table.shape[1] * plan.page_size:   # before memory for it is asked for
+            _check(1, "logmel_cache_evict")
+        kept = plan._empty((self.n_streams, plan.n_kv_heads, max(int(budget), 0)), dtype=plan._int32,
+                           device=plan.device)
         if stream is not None:
             kept.record_stream(stream)
-        _check(_lib.logmel_cache_evict(plan._h, self._view_ptr, to._view_ptr, int(budget), int(recent),
+        _check(_lib.logmel_cache_evict(plan._h, self._view_ptr, to._view_ptr, _int64(budget), _int64(recent),
                                        kept.data_ptr(), plan._stream(stream)), "logmel_cache_evict")
         return kept

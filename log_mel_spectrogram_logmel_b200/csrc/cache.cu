@@ -39,13 +39,17 @@ namespace {
   } while (0)
 
 // Makes the plan's device current for the call's launches and puts the
-// caller's back.
+// caller's back.  An error that is pending already is the call's: no launch is blamed for it.
 class DeviceScope {
  public:
-  explicit DeviceScope(int device) {
+  explicit DeviceScope(int device) : err_(cudaGetLastError()) {
     if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
-    if (prev_ != device) err_ = cudaSetDevice(device);
-    else prev_ = -1;
+    if (prev_ != device) {
+      const cudaError_t e = cudaSetDevice(device);
+      if (err_ == cudaSuccess) err_ = e;
+    } else {
+      prev_ = -1;
+    }
   }
   ~DeviceScope() {
     if (prev_ >= 0) cudaSetDevice(prev_);
@@ -54,7 +58,7 @@ class DeviceScope {
 
  private:
   int prev_ = -1;
-  cudaError_t err_ = cudaSuccess;
+  cudaError_t err_;
 };
 
 logmel_status check_config(const logmel_cache_config& c) {
@@ -230,6 +234,9 @@ size_t parts_bytes(const logmel_cache_plan* p) {
   return std::max(rows, chunk) * 2 * p->sms * sizeof(float);
 }
 
+// Join counters: one per warp of the few-rows kernel, eight per CTA of the weights kernel.
+size_t ticket_bytes(const logmel_cache_plan* p) { return sizeof(int) * (size_t)p->sms * std::max(ROWS_CTAS * ROWS_WARPS, 8); }
+
 template <typename T, int D>
 cudaError_t allow_shared_memory() {
   constexpr cudaFuncAttribute LIMIT = cudaFuncAttributeMaxDynamicSharedMemorySize;
@@ -357,7 +364,7 @@ logmel_status logmel_cache_plan_create(const logmel_cache_config* config, logmel
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->sms, cudaDevAttrMultiProcessorCount, p->device);
   if (e != cudaSuccess) return fail(record_cuda_error(e, "cudaDeviceGetAttribute", "cache.cu", __LINE__));
   if (!tensor_map_encoder()) return fail(record_cuda_error(cudaErrorNotSupported, "cuTensorMapEncodeTiled", "cache.cu", __LINE__));
-  const size_t tickets = sizeof(int) * (size_t)p->sms * ROWS_CTAS * ROWS_WARPS;
+  const size_t tickets = ticket_bytes(p);
   if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess || cudaMalloc(&p->d_tickets, tickets) != cudaSuccess ||
       cudaMalloc(&p->d_parts, parts_bytes(p)) != cudaSuccess ||
       cudaMalloc(&p->d_splits, sizeof(SplitItem) * p->sms) != cudaSuccess) {
@@ -536,6 +543,8 @@ logmel_status logmel_cache_evict(logmel_cache_plan* p, const logmel_cache_view* 
   const int64_t streams = cache->n_streams;
   if (streams == 0) return LOGMEL_OK;
   if (!kept || overlap(cache->lens, 4 * streams, to->lens, 4 * streams)) return LOGMEL_ERR_INVALID_ARG;
+  if (to->table == cache->table && (to->k_pages == cache->k_pages || to->v_pages == cache->v_pages || to->mass == cache->mass))
+    return LOGMEL_ERR_INVALID_ARG;   // the same pages
   if (budget > device_view(p, *to).capacity) return LOGMEL_ERR_INPUT_TOO_LONG;
   DeviceScope dev(p->device);
   CK(dev.error());
@@ -582,6 +591,8 @@ logmel_status logmel_cache_device_status(logmel_cache_plan* p, int* code, void* 
   CK(cudaMemcpyAsync(code, p->d_status, sizeof(int), cudaMemcpyDeviceToHost, str));
   CK(cudaMemsetAsync(p->d_status, 0, sizeof(int), str));
   CK(cudaStreamSynchronize(str));
+  // a call that gave up may have left its join counters behind
+  if (*code == LOGMEL_DEVICE_WAIT_TIMEOUT) CK(cudaMemsetAsync(p->d_tickets, 0, ticket_bytes(p), str));
   return LOGMEL_OK;
 }
 

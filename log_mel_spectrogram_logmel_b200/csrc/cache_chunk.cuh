@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
   int waves = 0, n_items = 0;
   if (a.b.uniform > 0) {
     const int64_t all = (int64_t)S * a.n_kv * ((a.b.uniform + item_tokens - 1) / item_tokens);
-    if (G <= MAX_CTAS && all >= G && all <= WAVES_MAX * G) {
+    if (G <= MAX_CTAS && all >= G && all <= WAVES_MAX * G && total < 0x7fffffff) {
       n_items = (int)all;
       waves = n_items / G;
     }
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
       int64_t own = 0;
       for (int w = 0; w < waves; ++w) own += place_of_item(a, w * G + tid).x.cost();
       over = own > quota;
-      bound[tid + 1] = (int)(quota - own);   // room left; below 2^31: a length is
+      bound[tid + 1] = (int)(quota - own);   // room left
     }
     if (__syncthreads_or(over)) {
       waves = 0;

@@ -206,8 +206,8 @@ __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
   return pack2(exp2_approx(y.x), exp2_approx(y.y));
 }
 
-// 2^x of two values on the FMA pipe, for finite x <= 100 or so; below -126
-// the result stays at 2^-126 (callers send masked and other infinite or NaN
+// 2^x of two values on the FMA pipe, for finite x: infinity from 128 on; below
+// -126 the result stays at 2^-126 (callers send masked and other infinite or NaN
 // values through ex2).  x = n + f with n the nearest integer (adding
 // 1.5 x 2^23 leaves n in the low bits), f in [-1/2, 1/2]; 2^f by the polynomial of
 // degree 4 of least relative error there (fitted by reweighted least squares,
@@ -217,7 +217,7 @@ __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
 // so a share of them goes this way.
 __device__ __forceinline__ uint64_t exp2_fit(uint64_t x) {
   const float2 y = unpack2(x);
-  const uint64_t z = pack2(fmaxf(y.x, -126.f), fmaxf(y.y, -126.f));
+  const uint64_t z = pack2(fminf(fmaxf(y.x, -126.f), 128.f), fminf(fmaxf(y.y, -126.f), 128.f));
   const uint64_t shift = pack2(12582912.f, 12582912.f), unshift = pack2(-12582912.f, -12582912.f);
   const uint64_t t = add2(z, shift);
   const uint64_t f = fma2(add2(t, unshift), pack2(-1.f, -1.f), z);

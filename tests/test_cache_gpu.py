@@ -275,6 +275,76 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them(lm, new, lens, 
                 assert torch.equal(out[~hit], want[~hit])
 
 
+@pytest.mark.parametrize("new,lens", [([2, 3], [40, 35]), ([100, 40], [130, 300]), ([300], [300])])
+def test_keys_that_are_nan_reach_the_rows_that_see_them(lm, new, lens):
+    for window in (0, 9):
+        for layout, dtype in (((16, 8, 128), torch.bfloat16), ((14, 2, 64), torch.float16)):
+            b = Box(lm, *layout, 16, dtype, new, lens)
+            want, tol, _, _ = b.attend_ref(window=window)
+            for back in sorted({0, 1, new[0] // 2, new[0] - 1, min(new[0] + 3, lens[0] - 1)}):
+                j = lens[0] - 1 - back
+                page = int(b.table[0, j // 16])
+                keep = b.k[page, 0, j % 16, 5].clone()
+                b.k[page, 0, j % 16, 5] = math.nan
+                out, lse = b.cache.attend(b.q, b.offsets, window=window, return_lse=True)
+                mass = b.mass.clone()
+                b.cache.weigh(b.q, torch.zeros_like(lse), b.offsets, window=window, out=mass)
+                b.k[page, 0, j % 16, 5] = keep
+                hit = torch.zeros_like(out, dtype=torch.bool)
+                hit[:new[0], :b.hq // b.hkv] = b.mask(0, True, window)[:, j][:, None, None]
+                assert torch.equal(out.isnan(), hit) and torch.equal(lse.isnan(), hit[:, :, 0]), (back, window)
+                assert bool((((out.double() - want).abs() <= tol) | hit).all())
+                live = torch.zeros_like(mass, dtype=torch.bool)
+                live[page, 0, j % 16] = True
+                assert torch.equal(mass.isnan(), live)
+
+
+def test_weights_past_the_largest_number(lm):
+    """An lse far below the scores gives infinity, not a wrapped exponent."""
+    for new, lens in (([1], [70]), ([140], [300])):
+        b = Box(lm, 16, 8, 128, 16, torch.bfloat16, new, lens)
+        lse = torch.full((b.rows, 16), -200.0, device="cuda")
+        out = b.mass.clone()
+        b.cache.weigh(b.q, lse, b.offsets, out=out)
+        live = b.live[:, 0, :, 0][:, None].expand_as(out)
+        assert bool((out[live] == math.inf).all()) and torch.equal(out[~live], b.mass[~live])
+
+
+def test_two_plans_at_once(lm):
+    """Calls on plans of their own may overlap on the GPU."""
+    boxes = [Box(lm, 16, 8, 128, 16, torch.bfloat16, new, lens, seed=i)
+             for i, (new, lens) in enumerate([([1] * 9, [700 + 90 * i for i in range(9)]), ([200, 40], [2000, 900]),
+                                              ([130], [5000]), ([1, 1], [9000, 40])])]
+    want = [b.check_attend() for b in boxes]
+    streams = [torch.cuda.Stream() for _ in boxes]
+    masses = [b.mass.clone() for b in boxes]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for b, st, m in zip(boxes, streams, masses):
+            with torch.cuda.stream(st):
+                out, lse = b.cache.attend(b.q, b.offsets, return_lse=True)
+                b.cache.weigh(b.q, lse, b.offsets, out=m)
+                got.append((out, lse))
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i % 4][0]) and torch.equal(lse, want[i % 4][1])
+    for b, m, (_, lse) in zip(boxes, masses, want):
+        again = b.mass.clone()
+        b.cache.weigh(b.q, lse, b.offsets, out=again)
+        assert torch.equal(m, again) and b.plan.device_status() == 0
+
+
+def test_many_heads_share_one(lm):
+    """64 query heads over one key head: a single token fills half a tile."""
+    for d, dtype in ((64, torch.float16), (128, torch.bfloat16)):
+        for new, lens in (([1, 1], [300, 4000]), ([3, 0, 9], [3, 9, 500])):
+            b = Box(lm, 64, 1, d, 32, dtype, new, lens)
+            b.check_attend()
+            b.check_attend(window=20)
+            b.check_weigh()
+
+
 def test_large_and_small_scores(lm):
     """One key carries everything; a key far below the others; equal scores; huge scores."""
     b = Box(lm, 16, 8, 128, 16, torch.bfloat16, [1, 20, 150], [600, 400, 300], sharp=40.0)
@@ -764,6 +834,10 @@ def test_refusals(lm):
         (lm.LogMelError, lambda: c.evict(lm.TokenCache.empty(b.plan, 2, 32), 32, recent=-1)),
         (lm.LogMelError, lambda: c.evict(lm.TokenCache.empty(b.plan, 3, 32), 32)),
         (lm.LogMelError, lambda: c.evict(lm.TokenCache(b.plan, b.k, b.v, b.table.clone(), b.lens, mass=b.mass), 32)),
+        (lm.LogMelError, lambda: c.evict(lm.TokenCache(b.plan, b.k, b.v, b.table, torch.zeros_like(b.lens), mass=b.mass), 32)),
+        (lm.LogMelError, lambda: c.evict(lm.TokenCache.empty(b.plan, 2, 32), 10 ** 30)),
+        (lm.LogMelError, lambda: c.attend(q, b.offsets, window=-10 ** 30)),
+        (lm.LogMelError, lambda: c.attend(q[:1].expand(3, -1, -1), b.offsets)),
         (TypeError, lambda: c.evict(None, 3)),
         (ValueError, lambda: c.evict(lm.TokenCache.empty(lm.CachePlan(16, 8, 64, 16), 2, 32), 3)),
         (TypeError, lambda: lm.TokenCache(b.plan, b.k.float(), b.v, b.table, b.lens)),
