@@ -571,7 +571,7 @@ logmel_status logmel_cache_evict(logmel_cache_plan* p, const logmel_cache_view* 
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t launch{};
     launch.gridDim = dim3(c.n_kv_heads * cluster, n);
-    launch.blockDim = dim3(SELECT_THREADS);
+    launch.blockDim = dim3(cluster > 1 ? SELECT_THREADS<true> : SELECT_THREADS<false>);
     launch.dynamicSmemBytes = 4 * (size_t)run;
     launch.stream = str;
     launch.attrs = &attr;

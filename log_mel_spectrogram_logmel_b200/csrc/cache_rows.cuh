@@ -161,7 +161,9 @@ __device__ __forceinline__ float slot_mass(const EvictArgs& a, int s, int h, int
 constexpr int SELECT_MAX_CLUSTER = 8;
 constexpr int SELECT_CACHED = 16384;   // slots of a run kept in shared memory
 
-constexpr int SELECT_THREADS = 512;
+// (256 for streams of one CTA: 8 of them an SM hide one another's steps)
+template <bool CLUSTER>
+constexpr int SELECT_THREADS = CLUSTER ? 512 : 256;
 
 struct SelectShared {
   int hist[2048];
@@ -173,7 +175,7 @@ struct SelectShared {
 };
 
 template <bool CLUSTER>
-__global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(SELECT_THREADS<CLUSTER>) select_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ uint32_t cached[];
   __shared__ SelectShared sh;
   namespace cg = cooperative_groups;
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(const __grid_con
     else __syncthreads();
   };
   const int h = blockIdx.x / C, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int THREADS = SELECT_THREADS, WARPS = THREADS / 32;
+  constexpr int THREADS = SELECT_THREADS<CLUSTER>, WARPS = THREADS / 32;
   const int len = a.c.length(s, tid == 0 && rank == 0);
   const int m = min(len, a.budget);
   const int newest = min(len, a.recent), old = len - newest;     // the other slots compete
