@@ -530,6 +530,13 @@ class CachePlan:
                "logmel_cache_rotary")
         return inv[:self.rotary_dim // 2], length.value
 
+    def _new(self, shape, dtype, stream):
+        """An output, from the memory of the stream that will write it."""
+        if stream is None:
+            return self._empty(shape, dtype=dtype, device=self.device)
+        with _torch().cuda.stream(stream):
+            return self._empty(shape, dtype=dtype, device=self.device)
+
     def _stream(self, stream):
         return self._current_stream(self._index) if stream is None else stream.cuda_stream
 
@@ -552,7 +559,9 @@ class TokenCache:
       lens              int32 [n_streams]: tokens of each stream, those of the push under way included
       mass              float32 [n_pages, n_kv_heads, page_size]: accumulated weights (weigh, evict)
 
-    lens, table and mass may be changed in place between calls (also inside a CUDA graph)."""
+    lens, table and mass may be changed in place between calls (also inside a
+    CUDA graph).  Calls take a stream (default: the current one); outputs that they
+    allocate belong to it, as if the call were made under torch.cuda.stream(stream)."""
 
     def __init__(self, plan: CachePlan, k_pages, v_pages, table, lens, mass=None):
         torch = _torch()
@@ -638,13 +647,6 @@ class TokenCache:
         # strides of dimensions of size one are never used
         return _Rows(t.data_ptr(), row if shape[0] > 1 else heads * plan.head_dim, head if heads > 1 else plan.head_dim)
 
-    def _new(self, rows, heads, stream):
-        plan = self.plan
-        out = plan._empty((rows, heads, plan.head_dim), dtype=plan.dtype, device=plan.device)
-        if stream is not None:
-            out.record_stream(stream)
-        return out
-
     def append(self, q, k, v, offsets=None, positions=None, q_out=None, stream=None):
         """Turns the new rows' queries and keys by their positions, and writes
         keys and values to the streams' newest slots (logmel_cache_append).  q is
@@ -667,7 +669,7 @@ class TokenCache:
                 raise ValueError("positions must hold one contiguous entry per row")
             pos = positions.data_ptr()
         if q_out is None:
-            q_out = self._new(rows, plan.n_q_heads, stream)
+            q_out = plan._new((rows, plan.n_q_heads, plan.head_dim), plan.dtype, stream)
         ro = self._rows(q_out, plan.n_q_heads, "q_out", rows)
         _check(_lib.logmel_cache_append(plan._h, self._view_ptr, off, ctypes.addressof(rq),
                                         ctypes.addressof(rk), ctypes.addressof(rv), pos, ctypes.addressof(ro),
@@ -685,13 +687,11 @@ class TokenCache:
         rows = q.shape[0]
         off, _held = self._offsets(offsets, rows)
         if out is None:
-            out = self._new(rows, plan.n_q_heads, stream)
+            out = plan._new((rows, plan.n_q_heads, plan.head_dim), plan.dtype, stream)
         ro = self._rows(out, plan.n_q_heads, "out", rows)
         lse = None
         if return_lse:
-            lse = plan._empty((rows, plan.n_q_heads), dtype=plan._float32, device=plan.device)
-            if stream is not None:
-                lse.record_stream(stream)
+            lse = plan._new((rows, plan.n_q_heads), plan._float32, stream)
         _check(_lib.logmel_cache_attend(plan._h, self._view_ptr, off, ctypes.addressof(rq),
                                         ctypes.addressof(ro), lse.data_ptr() if return_lse else None,
                                         int(bool(causal)), _int64(window), plan._stream(stream)),
@@ -736,10 +736,7 @@ class TokenCache:
             raise ValueError("to must have the layout of this cache")
         if budget > to.table.shape[1] * plan.page_size:   # before memory for it is asked for
             _check(1, "logmel_cache_evict")
-        kept = plan._empty((self.n_streams, plan.n_kv_heads, max(int(budget), 0)), dtype=plan._int32,
-                           device=plan.device)
-        if stream is not None:
-            kept.record_stream(stream)
+        kept = plan._new((self.n_streams, plan.n_kv_heads, max(int(budget), 0)), plan._int32, stream)
         _check(_lib.logmel_cache_evict(plan._h, self._view_ptr, to._view_ptr, _int64(budget), _int64(recent),
                                        kept.data_ptr(), plan._stream(stream)), "logmel_cache_evict")
         return kept
