@@ -303,7 +303,7 @@ logmel_status launch_attend(const logmel_cache_plan* p, const AttendArgs& a, int
     attend_chunk_kernel<T, D><<<p->sms, CHUNK_THREADS, ChunkShape<D>::SMEM, str>>>(x);
     const logmel_status st = launched(__LINE__);
     if (st != LOGMEL_OK) return st;
-    join_kernel<T, D><<<dim3(p->sms, ITEM_ROWS / JOIN_ROWS), JOIN_THREADS, 0, str>>>(x);
+    join_kernel<T, D><<<dim3(p->sms, ITEM_ROWS / JOIN_ROWS, JOIN_SLICES<D>), JOIN_THREADS, 0, str>>>(x);
   }
   return launched(__LINE__);
 }

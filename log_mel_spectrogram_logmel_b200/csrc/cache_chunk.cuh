@@ -824,55 +824,68 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
   if (warp == 9) tmem_free(tmem, 512);
 }
 
-// Joins the parts of split items: CTA (w, i) takes 32 rows of the item that
-// begins in run w, a lane per row and D / 8 columns per warp.
+// Joins the parts of split items: CTA (w, i, z) takes 32 rows of the item that
+// begins in run w and D / JOIN_SLICES of their columns, a lane per row and 8 columns per warp and
+// step.  Eight parts are under way at a time, with their maxima and sums.
 constexpr int JOIN_ROWS = 32;
 constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_BATCH = 8;
+
+template <int D>
+constexpr int JOIN_SLICES = D / 64;   // 64 columns a CTA: 8 for each of 8 warps
 
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ ChunkArgs a) {
-  constexpr int PART = ChunkShape<D>::PART, PIECES = D / 32;   // pieces of 4 columns per warp
+  constexpr int PART = ChunkShape<D>::PART;
   const int first = blockIdx.x;
   const SplitItem x = a.splits[first];
-  const int r = blockIdx.y * JOIN_ROWS + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+  const int r = blockIdx.y * JOIN_ROWS + (threadIdx.x & 31), piece = blockIdx.z * 16 + 2 * (threadIdx.x >> 5);   // of 4 columns
   const int tk = (r & 127) / a.group, j = (r >> 7) * a.tokens + tk;
   if (x.last < 0 || tk >= a.tokens || j >= x.count) return;
   auto slot = [&](int w) { return a.parts + (int64_t)(2 * w + (w == first ? 1 : 0)) * PART; };
-  float mm = -INFINITY;
-#pragma unroll 4
-  for (int w = first; w <= x.last; ++w) mm = fmaxf(mm, __ldcg(slot(w) + r));
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float4 acc[PIECES];
-  float sum = 0.f;
+  float m = -INFINITY, sum = 0.f, acc[8] = {};
+  for (int w0 = first; w0 <= x.last; w0 += JOIN_BATCH) {
+    float pm[JOIN_BATCH], pl[JOIN_BATCH];
+    float4 y[JOIN_BATCH][2];
 #pragma unroll
-  for (int e = 0; e < PIECES; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int w = first; w <= x.last; ++w) {
-    const float* sl = slot(w);
-    const float f = exp2_approx(__ldcg(sl + r) - base);
-    sum += f * __ldcg(sl + ITEM_ROWS + r);
+    for (int i = 0; i < JOIN_BATCH; ++i) {
+      const bool there = w0 + i <= x.last;
+      const float* sl = slot(there ? w0 + i : first);
+      pm[i] = there ? __ldcg(sl + r) : -INFINITY;
+      pl[i] = there ? __ldcg(sl + ITEM_ROWS + r) : 0.f;
 #pragma unroll
-    for (int e = 0; e < PIECES; ++e) {
-      const float4 y = __ldcg((const float4*)(sl + 2 * ITEM_ROWS) + (PIECES * warp + e) * ITEM_ROWS + r);
-      acc[e].x += f * y.x;
-      acc[e].y += f * y.y;
-      acc[e].z += f * y.z;
-      acc[e].w += f * y.w;
+      for (int e = 0; e < 2; ++e)
+        y[i][e] = there ? __ldcg((const float4*)(sl + 2 * ITEM_ROWS) + (piece + e) * ITEM_ROWS + r) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < JOIN_BATCH; ++i) top = fmaxf(top, pm[i]);
+    const float base = top == -INFINITY ? 0.f : top, old = exp2_approx(m - base);   // 0 while m is minus infinity
+    m = top;
+    sum *= old;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= old;
+#pragma unroll
+    for (int i = 0; i < JOIN_BATCH; ++i) {
+      const float f = exp2_approx(pm[i] - base);
+      sum += f * pl[i];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        acc[4 * e] += f * y[i][e].x;
+        acc[4 * e + 1] += f * y[i][e].y;
+        acc[4 * e + 2] += f * y[i][e].z;
+        acc[4 * e + 3] += f * y[i][e].w;
+      }
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t tr = a.b.begin(x.s) + x.i0 + j;
   const int head = x.h * a.group + (r & 127) - tk * a.group;
-  T* out = (T*)a.out.data + tr * a.out.row + (int64_t)head * a.out.head + 4 * PIECES * warp;
-#pragma unroll
-  for (int e = 0; e < PIECES; e += 2) {
-    uint4 w = make_uint4(Half2<T>::from_float(acc[e].x * inv, acc[e].y * inv), Half2<T>::from_float(acc[e].z * inv, acc[e].w * inv),
-                         Half2<T>::from_float(acc[e + 1].x * inv, acc[e + 1].y * inv),
-                         Half2<T>::from_float(acc[e + 1].z * inv, acc[e + 1].w * inv));
-    if (sum == 0.f) w = make_uint4(0u, 0u, 0u, 0u);
-    *(uint4*)(out + 4 * e) = w;
-  }
-  if (a.lse && warp == 0) a.lse[tr * a.n_q + head] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * LN2;
+  uint4 w = make_uint4(Half2<T>::from_float(acc[0] * inv, acc[1] * inv), Half2<T>::from_float(acc[2] * inv, acc[3] * inv),
+                       Half2<T>::from_float(acc[4] * inv, acc[5] * inv), Half2<T>::from_float(acc[6] * inv, acc[7] * inv));
+  if (sum == 0.f) w = make_uint4(0u, 0u, 0u, 0u);
+  *(uint4*)((T*)a.out.data + tr * a.out.row + (int64_t)head * a.out.head + 4 * piece) = w;
+  if (a.lse && piece == 0) a.lse[tr * a.n_q + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2;
 }
 
 }  // namespace cache
