@@ -287,7 +287,7 @@ logmel_status launched(int line) {
 
 template <typename T, int D>
 logmel_status launch_attend(const logmel_cache_plan* p, const AttendArgs& a, int64_t most, cudaStream_t str) {
-  if (most * p->group <= ROWS_TILE) {
+  if (most * p->group <= ROWS_MOST<D>) {
     attend_rows_kernel<T, D><<<p->sms * ROWS_CTAS, ROWS_WARPS * 32, RowsShape<D>::SMEM, str>>>(a);
   } else {
     ChunkArgs x;

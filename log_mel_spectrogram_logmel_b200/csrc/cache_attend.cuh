@@ -1,7 +1,7 @@
 // Token cache: attention of new rows over the cached slots.
 //
 // attend_rows_kernel serves pushes of few rows (new tokens x query heads of a
-// key head <= 16 in every stream), where every cached byte is used by a
+// key head <= ROWS_MOST<D> in every stream), where every cached byte is used by a
 // handful of rows and memory traffic is the bound.
 #pragma once
 #include "cache_tensor.cuh"
@@ -24,9 +24,10 @@ struct AttendArgs {
 // ---------------------------------------------------------------------------
 // few rows
 // ---------------------------------------------------------------------------
-// The rows of one (stream, key head) fill one 16-row tensor-core tile; its
+// The rows of one (stream, key head) fill one 16-row tensor-core tile, or two
+// that read the same keys one after the other's warps (from L2); its
 // keys are cut into units of 8 KB (16 keys of 128 dimensions, 32 of 64).  All units of the launch form one line,
-// (stream, key head, unit), which is cut into equal runs, one per warp: every
+// (stream, key head, tile, unit), which is cut into equal runs, one per warp: every
 // warp gets the same number of bytes whatever the lengths are, and no host
 // knowledge of the lengths is needed.  A warp copies its units through a ring
 // of its own with cp.async (no barrier with other warps; the ring runs ahead
@@ -34,6 +35,10 @@ struct AttendArgs {
 // flight.  Rows whose keys end up in several warps are joined by the last of
 // them to finish, in the order of the units, so results do not depend on timing.
 constexpr int ROWS_TILE = 16;
+// Rows of a push that this kernel takes; more go to the chunk kernel.  256 streams of 21 rows of 64 dimensions take 84 us
+// here and 110 there (56 rows: 141 and 112), 64 streams of 24 rows of 128 dimensions 160 us here and 134 there.
+template <int D>
+constexpr int ROWS_MOST = D == 64 ? 32 : 16;
 constexpr int ROWS_WARPS = 4;
 constexpr int ROWS_CTAS = 2;                  // per SM
 constexpr int ROWS_MIN_UNITS = 4;             // a shorter run costs more in joining than it saves
@@ -87,7 +92,9 @@ __device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, ui
 // that rows that see nothing are still written.
 struct Extent {
   int n, len, lo, hi, first, units;
-  __device__ int line() const { return units == 0 ? 0 : units + ROWS_ITEM_COST; }
+  int tiles;   // of 16 rows
+  __device__ int item() const { return units + ROWS_ITEM_COST; }            // places of a tile of rows on the line
+  __device__ int line() const { return units == 0 ? 0 : item() * tiles; }
 };
 
 __device__ __forceinline__ Extent extent_of(const AttendArgs& a, int s, int shift, bool report) {
@@ -97,13 +104,14 @@ __device__ __forceinline__ Extent extent_of(const AttendArgs& a, int s, int shif
   e.lo = seen(e.len, e.n, 0, a.causal, a.window).x;
   e.hi = e.len;
   e.first = e.lo >> shift;
+  e.tiles = (e.n * a.group + ROWS_TILE - 1) / ROWS_TILE;
   e.units = e.n == 0 ? 0 : max(1, ((e.hi + (1 << shift) - 1) >> shift) - e.first);
   return e;
 }
 
 // A place on the line of units.
 struct Place {
-  int s, h, unit;    // unit counts from the item's first
+  int s, h, tile, unit;    // unit counts from the item's first
   Extent e;
 };
 
@@ -163,7 +171,9 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
       u += here;
     }
     at.h = (int)((u0 - u) / at.e.line());
-    at.unit = (int)(u0 - u - (int64_t)at.h * at.e.line()) - ROWS_ITEM_COST;
+    const int left = (int)(u0 - u - (int64_t)at.h * at.e.line());
+    at.tile = left / at.e.item();
+    at.unit = left - at.tile * at.e.item() - ROWS_ITEM_COST;
     if (at.unit < 0) {   // among the places that stand for the item's start
       u0 -= at.unit;
       at.unit = 0;
@@ -174,6 +184,8 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
   auto step = [&](Place& p) {   // to the next unit of the line (which exists)
     if (++p.unit < p.e.units) return;
     p.unit = 0;
+    if (++p.tile < p.e.tiles) return;
+    p.tile = 0;
     if (++p.h < a.n_kv) return;
     p.h = 0;
     do p.e = extent_of(a, ++p.s, Shape::SHIFT, false);
@@ -263,14 +275,15 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
   const T* qrow[2];
 
   auto begin_item = [&] {
-    rows = at.e.n * a.group;
+    rows = min(ROWS_TILE, at.e.n * a.group - at.tile * ROWS_TILE);
     const int64_t t0 = a.b.begin(at.s);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = gr + 8 * i;
-      const bool valid = r < rows;
+      const bool valid = gr + 8 * i < rows;
+      const int r = at.tile * ROWS_TILE + gr + 8 * i;   // of all the push's
       const int tok = valid ? r / a.group : 0;
-      qrow[i] = (const T*)a.q.data + (t0 + tok) * a.q.row + (int64_t)(at.h * a.group + r - tok * a.group) * a.q.head;
+      qrow[i] = (const T*)a.q.data + (t0 + tok) * a.q.row +
+                (valid ? (int64_t)(at.h * a.group + r - tok * a.group) * a.q.head : 0);
       row_seen[i] = valid ? seen(at.e.len, at.e.n, tok, a.causal, a.window) : make_int2(0, 0);
 #pragma unroll
       for (int j = 0; j < KSTEPS; ++j) {
@@ -433,9 +446,8 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
     if (item_done && from_start) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = gr + 8 * i;
-        if (r >= rows) continue;
-        const int tok = r / a.group, hq = at.h * a.group + r - tok * a.group;
+        if (gr + 8 * i >= rows) continue;
+        const int r = at.tile * ROWS_TILE + gr + 8 * i, tok = r / a.group, hq = at.h * a.group + r - tok * a.group;
         const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
         T* out = (T*)a.out.data + (t0 + tok) * a.out.row + (int64_t)hq * a.out.head;
 #pragma unroll
@@ -470,7 +482,7 @@ __global__ void __launch_bounds__(ROWS_WARPS * 32, ROWS_CTAS) attend_rows_kernel
         auto slot = [&](int w) { return a.parts + (int64_t)(2 * w + (w == first ? 1 : 0)) * Shape::PART; };
         constexpr int V = D / 32;   // columns of a lane
         auto write_row = [&](int r, const float* acc, float sum, float mm) {
-          const int tok = r / a.group, hq = at.h * a.group + r - tok * a.group;
+          const int all = at.tile * ROWS_TILE + r, tok = all / a.group, hq = at.h * a.group + all - tok * a.group;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           T* out = (T*)a.out.data + (t0 + tok) * a.out.row + (int64_t)hq * a.out.head;
 #pragma unroll
