@@ -513,9 +513,17 @@ logmel_status logmel_cache_evict(logmel_cache_plan* plan, const logmel_cache_vie
                                  const logmel_cache_view* to, int64_t budget, int64_t recent, int32_t* kept,
                                  void* stream);
 
+/* Test hook for the bounded waits inside the cache's tiled kernels (not for
+ * normal use): extra_tx_bytes (a multiple of 16, at most 512 KiB) is added to the
+ * bytes that the barrier of the query copies expects.  Every real copy is still issued and
+ * lands, but the barrier never completes, so the waits run out after about a
+ * second; the call stores LOGMEL_DEVICE_WAIT_TIMEOUT and ends, and the context stays
+ * usable.  0 restores normal operation.  Host only. */
+logmel_status logmel_cache_plan_set_wait_test(logmel_cache_plan* plan, int extra_tx_bytes);
+
 /* Reads and clears the plan's device status word (synchronises `stream`):
  * 0, LOGMEL_DEVICE_BAD_CACHE or LOGMEL_DEVICE_WAIT_TIMEOUT (a bounded wait
- * inside a kernel ran out, about 0.3 s: the results of the calls since the
+ * inside a kernel ran out, about a second: the results of the calls since the
  * last read are not complete). */
 logmel_status logmel_cache_device_status(logmel_cache_plan* plan, int* code, void* stream);
 

@@ -121,6 +121,7 @@ _SIGS = {
     "logmel_cache_weigh": (_i, [_p, _vp, _vp, _vp, _vp, _i, _i64, _f, _vp, _vp]),
     "logmel_cache_evict": (_i, [_p, _vp, _vp, _i64, _i64, _vp, _vp]),
     "logmel_cache_device_status": (_i, [_p, ctypes.POINTER(_i), _vp]),
+    "logmel_cache_plan_set_wait_test": (_i, [_p, _i]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -529,6 +530,12 @@ class CachePlan:
         _check(_lib.logmel_cache_rotary(ctypes.addressof(self._config), inv.ctypes.data, ctypes.addressof(length)),
                "logmel_cache_rotary")
         return inv[:self.rotary_dim // 2], length.value
+
+    def set_wait_test(self, extra_tx_bytes: int) -> None:
+        """Test hook (logmel_cache_plan_set_wait_test): make the bounded waits
+        of the tiled kernels run out (extra expected bytes that never arrive); 0 restores
+        normal operation."""
+        _check(_lib.logmel_cache_plan_set_wait_test(self._h, int(extra_tx_bytes)), "logmel_cache_plan_set_wait_test")
 
     def _new(self, shape, dtype, stream):
         """An output, from the memory of the stream that will write it."""

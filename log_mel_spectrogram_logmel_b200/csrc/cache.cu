@@ -24,6 +24,7 @@ struct logmel_cache_plan {
   int device = 0, sms = 0, page_shift = 0, group = 1;
   float scale = 0.f;
   RotaryArgs rotary{};
+  int tx_extra = 0;           // bounded waits (test hook; 0 in normal operation)
   int* d_status = nullptr;
   int* d_tickets = nullptr;   // split rows: one counter per worker, zero between calls
   float* d_parts = nullptr;   // split rows: two partial tiles per worker
@@ -300,6 +301,7 @@ logmel_status launch_attend(const logmel_cache_plan* p, const AttendArgs& a, int
         !encode_pages(p, &x.v_map, c.v, c.n_pages, c.v_page, c.v_head, c.v_slot, x.box_keys))
       return no_map(__LINE__);
     x.splits = p->d_splits;
+    x.tx_extra = p->tx_extra;
     attend_chunk_kernel<T, D><<<p->sms, CHUNK_THREADS, ChunkShape<D>::SMEM, str>>>(x);
     const logmel_status st = launched(__LINE__);
     if (st != LOGMEL_OK) return st;
@@ -312,6 +314,7 @@ template <typename T, int D, int N>
 logmel_status launch_weigh_columns(const logmel_cache_plan* p, WeighArgs& a, cudaStream_t str) {
   a.tokens = N / p->group;
   a.box_keys = std::min(p->cfg.page_size, TILE_KEYS);
+  a.tx_extra = p->tx_extra;
   const CacheView& c = a.c;
   if (!encode_rows(p, &a.q_map, a.q, a.b.rows, a.n_q, a.tokens) ||
       !encode_pages(p, &a.k_map, c.k, c.n_pages, c.k_page, c.k_head, c.k_slot, a.box_keys))
@@ -580,6 +583,13 @@ logmel_status logmel_cache_evict(logmel_cache_plan* p, const logmel_cache_view* 
     gather_kernel<<<dim3((unsigned)((budget + GATHER_ROWS - 1) / GATHER_ROWS), c.n_kv_heads, n), GATHER_THREADS, 0, str>>>(a);
     if ((st = launched(__LINE__)) != LOGMEL_OK) return st;
   }
+  return LOGMEL_OK;
+}
+
+logmel_status logmel_cache_plan_set_wait_test(logmel_cache_plan* p, int extra_tx_bytes) {
+  // a barrier counts at most 2^20 - 1 bytes of one phase, and a step's queries are up to 64 KB of them
+  if (!p || extra_tx_bytes < 0 || extra_tx_bytes % 16 || extra_tx_bytes > (1 << 19)) return LOGMEL_ERR_INVALID_ARG;
+  p->tx_extra = extra_tx_bytes;
   return LOGMEL_OK;
 }
 

@@ -59,6 +59,7 @@ struct SplitItem {
 struct ChunkArgs : AttendArgs {
   CUtensorMap q_map, k_map, v_map;
   SplitItem* splits;   // one per CTA
+  int tx_extra;        // test hook: bytes that never arrive
   int tokens;      // tokens of a tile: 128 / group
   int box_keys;    // slots a key copy brings: min(page size, 128)
 };
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1) attend_chunk_kernel(const __
           ++q_uses;
           if (lane == 0) {
             const int row = a.b.begin(p.s) + p.x.i0;
-            mbar_expect(q_full, tiles * HALVES * a.tokens * a.group * 128);
+            mbar_expect(q_full, tiles * HALVES * a.tokens * a.group * 128 + a.tx_extra);
             for (int i = 0; i < tiles; ++i)
               for (int c = 0; c < HALVES; ++c)
                 tma_load_3d(q_smem + i * TILE + c * HALF_TILE, &a.q_map, 64 * c, p.h * a.group, row + i * a.tokens, q_full);

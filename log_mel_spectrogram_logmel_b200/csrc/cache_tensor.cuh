@@ -43,7 +43,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
-// Every wait is bounded (2^18 polls of about a microsecond).  One that runs
+// Every wait is bounded (2^18 polls, about a second).  One that runs
 // out raises the CTA's `stop` word and the plan's status; the other roles
 // see `stop` and leave their loops too.
 constexpr int WAIT_POLLS = 1 << 18;

@@ -38,6 +38,7 @@ struct WeighArgs {
   int* tickets;        // eight per CTA, zero between calls
   float* parts;        // sums of split items, two per CTA
   CUtensorMap q_map, k_map;
+  int tx_extra;        // test hook: bytes that never arrive
   int tokens;          // tokens of a step: N / group
   int box_keys;        // slots a key copy brings
 };
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(WeighShape<D, N>::THREADS, 1) weigh_kernel(con
         for (int i = x.i0; i < x.i1 && ok; ++i) {
           if (!(ok = mbar_wait(q_free(qs), q_phase ^ 1, stop, status))) break;
           if (elect_lane()) {
-            mbar_expect(q_full(qs), HALVES * a.tokens * a.group * 128);
+            mbar_expect(q_full(qs), HALVES * a.tokens * a.group * 128 + a.tx_extra);
             for (int c = 0; c < HALVES; ++c)
               tma_load_3d(q_ring + qs * Shape::Q_TILE + c * Q_HALF, &a.q_map, 64 * c, x.h * a.group, row + i * a.tokens,
                           q_full(qs));

@@ -68,6 +68,7 @@ def test_null_arguments_are_refused():
     assert lm._lib.logmel_cache_attend(None, None, None, None, None, None, 1, 0, None) == 1
     assert lm._lib.logmel_cache_weigh(None, None, None, None, None, 1, 0, 1.0, None, None) == 1
     assert lm._lib.logmel_cache_evict(None, None, None, 1, 0, None, None) == 1
+    assert lm._lib.logmel_cache_plan_set_wait_test(None, 0) == 1
     lm._lib.logmel_cache_plan_destroy(None)
 
 

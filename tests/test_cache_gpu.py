@@ -803,6 +803,28 @@ def test_bad_tables_and_lengths_are_reported_not_followed(lm, new):
     assert b.plan.device_status() == 4
 
 
+def test_waits_that_run_out_are_reported(lm):
+    """Copies that never complete a barrier: the calls end, the status word says so, the next calls are right."""
+    b = Box(lm, 16, 8, 128, 16, torch.bfloat16, [90, 1, 20], [300, 120, 777])
+    want, lse = b.check_attend()
+    masses = b.mass.clone()
+    b.cache.weigh(b.q, lse, b.offsets, out=masses)
+    for bad in (-16, 8, (1 << 19) + 16):
+        with pytest.raises(lm.LogMelError):
+            b.plan.set_wait_test(bad)
+    for call in (lambda: b.cache.attend(b.q, b.offsets), lambda: b.cache.weigh(b.q, lse, b.offsets, out=b.mass.clone())):
+        b.plan.set_wait_test(16)
+        call()
+        b.plan.set_wait_test(0)
+        assert b.plan.device_status() == 5
+        assert b.plan.device_status() == 0
+        out, got = b.cache.attend(b.q, b.offsets, return_lse=True)
+        again = b.mass.clone()
+        b.cache.weigh(b.q, lse, b.offsets, out=again)
+        assert torch.equal(out, want) and torch.equal(got, lse) and torch.equal(again, masses)
+        assert b.plan.device_status() == 0
+
+
 def test_refusals(lm):
     b = Box(lm, 16, 8, 128, 16, torch.bfloat16, [1, 2], [30, 40], rotary_dim=128)
     c, q = b.cache, b.q
