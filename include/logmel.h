@@ -524,7 +524,8 @@ logmel_status logmel_cache_plan_set_wait_test(logmel_cache_plan* plan, int extra
 /* Reads and clears the plan's device status word (synchronises `stream`):
  * 0, LOGMEL_DEVICE_BAD_CACHE or LOGMEL_DEVICE_WAIT_TIMEOUT (a bounded wait
  * inside a kernel ran out, about a second: the results of the calls since the
- * last read are not complete). */
+ * last read are not complete, and later calls are right only after this
+ * read); the larger of the two where both occurred. */
 logmel_status logmel_cache_device_status(logmel_cache_plan* plan, int* code, void* stream);
 
 /* Test hook for the bounded wait on a tile's span copies (not for normal

@@ -525,7 +525,7 @@ class CachePlan:
     def _rotary(self):
         inv = np.zeros(max(self.rotary_dim // 2, 1), np.float64)
         length = ctypes.c_double(1.0)
-        if self.rotary_dim > 2 * 64:
+        if not 0 <= self.rotary_dim <= 128:   # what inv holds, whatever ctypes makes of the value
             _check(2, "logmel_cache_rotary")
         _check(_lib.logmel_cache_rotary(ctypes.addressof(self._config), inv.ctypes.data, ctypes.addressof(length)),
                "logmel_cache_rotary")

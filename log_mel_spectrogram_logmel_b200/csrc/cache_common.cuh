@@ -57,7 +57,8 @@ struct CacheView {
   int page_shift;
   int* status;
 
-  __device__ void flag() const { atomicExch(status, LOGMEL_DEVICE_BAD_CACHE); }
+  // the larger code stays: a wait that ran out must not be hidden, the plan's counters depend on it
+  __device__ void flag() const { atomicMax(status, LOGMEL_DEVICE_BAD_CACHE); }
   // lens[s], clamped to what the table holds
   __device__ int length(int s, bool report) const {
     const int len = lens[s];

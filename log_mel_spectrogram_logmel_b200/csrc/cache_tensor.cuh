@@ -55,7 +55,7 @@ __device__ __forceinline__ bool mbar_wait_thread(uint32_t bar, uint32_t parity, 
     if ((i & 15) == 15 && *stop) return false;
   }
   *stop = 1;
-  atomicExch(status, LOGMEL_DEVICE_WAIT_TIMEOUT);
+  atomicMax(status, LOGMEL_DEVICE_WAIT_TIMEOUT);
   return false;
 }
 

@@ -823,6 +823,16 @@ def test_waits_that_run_out_are_reported(lm):
         b.cache.weigh(b.q, lse, b.offsets, out=again)
         assert torch.equal(out, want) and torch.equal(got, lse) and torch.equal(again, masses)
         assert b.plan.device_status() == 0
+    # a bad length after it does not hide it
+    b.plan.set_wait_test(16)
+    b.cache.attend(b.q, b.offsets)
+    b.plan.set_wait_test(0)
+    good = b.cache.lens.clone()
+    b.cache.lens[0] = -1
+    b.cache.attend(b.q, b.offsets)
+    b.cache.lens.copy_(good)
+    assert b.plan.device_status() == 5
+    assert torch.equal(b.cache.attend(b.q, b.offsets), want)
 
 
 def test_refusals(lm):
