@@ -334,7 +334,9 @@ __global__ void __launch_bounds__(GATHER_THREADS) gather_kernel(const __grid_con
   for (int u = threadIdx.x; u < rows * per_row; u += GATHER_THREADS) {
     const int r = u / per_row, x = (u - r * per_row) * 8;
     const int from = kept[r], at = r0 + r;
-    const int p = a.c.page(s, from >> a.c.page_shift), q = a.to.page(s, at >> a.to.page_shift);
+    const int q = a.to.page(s, at >> a.to.page_shift);
+    // (weights that change while the call runs can leave an entry of `kept` unwritten)
+    const int p = (unsigned)from < (unsigned)len ? a.c.page(s, from >> a.c.page_shift) : -1;
     if (p < 0 || q < 0) {
       a.c.flag();
       continue;
