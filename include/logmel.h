@@ -424,7 +424,7 @@ typedef struct {
   double rotary_factor; /* LINEAR: angles divided by it; RAMP: pairs below one turn in rotary_context are,
                          * pairs above 32 turns are not, those between in proportion to their index, and turned
                          * pairs are 0.1 ln(factor) + 1 times as long */
-  double softmax_scale; /* factor on q . k; 0: 1 / sqrt(head_dim) */
+  double softmax_scale; /* factor on q . k, a normal fp32 number below 1.7e38; 0: 1 / sqrt(head_dim) */
 } logmel_cache_config;
 
 typedef struct {

@@ -75,8 +75,9 @@ logmel_status check_config(const logmel_cache_config& c) {
   if (c.rotary_scaling != LOGMEL_ROTARY_PLAIN && (!(c.rotary_factor >= 1.0) || !std::isfinite(c.rotary_factor)))
     return LOGMEL_ERR_INVALID_ARG;
   if (c.rotary_scaling == LOGMEL_ROTARY_RAMP && c.rotary_context < 1) return LOGMEL_ERR_INVALID_ARG;
-  // the kernels hold scale * log2(e) in fp32
+  // the kernels hold scale * log2(e) in fp32, and multiply the minus infinity of an unseen slot by it
   if (!(c.softmax_scale >= 0.0) || !std::isfinite((float)(c.softmax_scale * 2.0))) return LOGMEL_ERR_INVALID_ARG;
+  if (c.softmax_scale > 0.0 && c.softmax_scale < std::numeric_limits<float>::min()) return LOGMEL_ERR_INVALID_ARG;
   return LOGMEL_OK;
 }
 

@@ -52,7 +52,8 @@ def test_ramp_keeps_fast_pairs_and_slows_the_slow_ones():
     (dict(rotary_dim=-16), 2), (dict(rotary_scaling=3), 2), (dict(rotary_base=1.0), 1),
     (dict(rotary_base=math.inf), 1), (dict(rotary_base=math.nan), 1), (dict(rotary_scaling=1, rotary_factor=0.5), 1),
     (dict(rotary_scaling=2, rotary_factor=2.0, rotary_context=0), 1), (dict(softmax_scale=-1.0), 1),
-    (dict(softmax_scale=math.nan), 1), (dict(softmax_scale=1e39), 1), (dict(softmax_scale=3e38), 1)])
+    (dict(softmax_scale=math.nan), 1), (dict(softmax_scale=1e39), 1), (dict(softmax_scale=3e38), 1),
+    (dict(softmax_scale=1e-46), 1)])
 def test_bad_configurations_are_refused(change, code):
     assert _rotary(**change)[0] == code
     c = lm._CacheConfig(**{**CONFIG, **change})
